@@ -74,7 +74,8 @@ typedef enum {
                                      dependency wait of a tree sweep gave up (info = -2) */
 } selinv_status;
 
-typedef enum { SELINV_F64 = 0, SELINV_F32 = 1 } selinv_dtype;
+/* SELINV_BF16 and SELINV_F16 are element types of the sequence operators only. */
+typedef enum { SELINV_F64 = 0, SELINV_F32 = 1, SELINV_BF16 = 2, SELINV_F16 = 3 } selinv_dtype;
 
 /* Human-readable name of a status code (static string). */
 const char *selinv_status_string(selinv_status s);
@@ -475,6 +476,159 @@ selinv_status selinv_tree_backward(const selinv_tree_plan_t *plan, selinv_dtype 
                                    const void *G_edge, const void *Gb_diag, const void *Gb_edge,
                                    void *Db, void *Eb, int32_t *info, void *workspace,
                                    size_t workspace_bytes, void *stream);
+
+/*
+ * ---- Sequence operators ----------------------------------------------------
+ *
+ * The state-space layer along chains: a selective scan -- the solve of a block
+ * lower-bidiagonal system (the non-symmetric chain of selinv_bidiag) with
+ * M_tt = I and M_{t,t-1} = -diag(a_t) whose blocks depend on the row -- and the
+ * short causal convolution in front of it, for prompts, training and single
+ * tokens.
+ *
+ * Conventions that differ from the block arrays above
+ *   - dtype is the element type of x, dt, z, B, C, y (convolution: x, weight,
+ *     bias, states, y) and of their cotangents: SELINV_F64, SELINV_F32,
+ *     SELINV_BF16 or SELINV_F16.  Arithmetic, sums, the scan's states and
+ *     parameters (A, D, dt_bias) and every parameter's cotangent are float64
+ *     for SELINV_F64 and float32 otherwise ("arithmetic type").
+ *   - Arrays [lines, rows, d] come as a selinv_view: channels are contiguous,
+ *     the strides between rows and lines are the caller's (in elements, not
+ *     negative; inputs may overlap or repeat, outputs may not).  16-byte
+ *     alignment of base and strides enables the vectorised paths.
+ *   - Without a table each line is one sequence of `rows` rows.  With a table
+ *     there is one line, holding the sequences one after another: `table`
+ *     (device, int64, 1 + live + sequences entries) has the first rows of the
+ *     `live` sequences that have any, ascending, then `rows`, then the numbers
+ *     of those sequences, then the numbers of the sequences without rows.
+ *     States are [lines or sequences, ...], in the order of those numbers.  A
+ *     sequence without rows ends in the state it begins with.
+ *   - Results do not depend on timing: every sum has one order.
+ *   - No info[] but for the steps': there is no input for which these fail.
+ */
+typedef struct {
+    const void *data;         /* outputs are written through it as well */
+    int64_t line, row;        /* strides in elements */
+} selinv_view;
+
+#define SELINV_SOFTPLUS 1     /* flags: dt' = softplus(dt + dt_bias) */
+#define SELINV_SILU 2         /* flags: the convolution's silu */
+
+/*
+ * Selective scan.  For every line, channel c of d, state m of n and group
+ * g = c / (d / groups):
+ *   dt'_t = dt_t + dt_bias, its softplus with SELINV_SOFTPLUS
+ *   h_t[m] = exp(dt'_t A[c, m]) h_{t-1}[m] + dt'_t x_t B_t[g, m]
+ *   y_t = (sum_m C_t[g, m] h_t[m] + D x_t) * z_t sigmoid(z_t)
+ * Limits: n <= 64, d <= 2^20, d a multiple of groups.
+ */
+typedef struct {
+    int64_t dtype, flags;             /* SELINV_SOFTPLUS or 0 */
+    int64_t lines, rows, d, n, groups;
+    int64_t sequences, live;          /* with a table */
+    const int64_t *table;             /* or NULL */
+    selinv_view x, dt, z, B, C;       /* z.data may be NULL (no gate); B, C [lines, rows, groups, n] */
+    int64_t B_group, C_group;         /* strides between groups */
+    const void *A;                    /* [d, n] */
+    const void *D, *dt_bias;          /* [d] or NULL (zero) */
+    const void *state;                /* initial states [lines or sequences, d, n], or NULL (zero) */
+} selinv_scan_inputs;
+
+/* Bytes of the states that selinv_selective_scan keeps for the backward: one [d, n] per 16 rows of a line. */
+size_t selinv_selective_scan_kept_size(const selinv_scan_inputs *a);
+size_t selinv_selective_scan_workspace_size(const selinv_scan_inputs *a);
+size_t selinv_selective_scan_backward_workspace_size(const selinv_scan_inputs *a);
+
+/*
+ * Writes y [lines, rows, d], where not NULL the final states state_out
+ * (layout of `state`; must not overlap it) and the states `kept`.
+ * Workspace: selinv_selective_scan_workspace_size(a) bytes (0 when the channels
+ * fill the GPU: lines are cut into segments only when they do not).
+ */
+selinv_status selinv_selective_scan(const selinv_scan_inputs *a, const selinv_view *y, void *state_out, void *kept,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Cotangents of selinv_selective_scan.  yb is y's, stateb the final states'
+ * (NULL = zero); kept comes from the forward on the same inputs.  Writes xb,
+ * dtb, zb (when z is given), Bb, Cb, Ab [d, n], and where not NULL Db [d],
+ * dt_biasb [d] and stateb_out, the initial states' (layout of `state`).
+ */
+typedef struct {
+    const void *kept;
+    selinv_view yb;
+    const void *stateb;
+    selinv_view xb, dtb, zb, Bb, Cb;
+    int64_t Bb_group, Cb_group;
+    void *Ab, *Db, *dt_biasb, *stateb_out;
+} selinv_scan_grads;
+selinv_status selinv_selective_scan_backward(const selinv_scan_inputs *a, const selinv_scan_grads *g, void *workspace,
+                                             size_t workspace_bytes, void *stream);
+
+/*
+ * Selective scan for single tokens: row r of [batch, ...] continues the state
+ * cache[index[r]] (cache [slots, d, n]; index NULL: slot r), which goes to the
+ * same slot of cache_out (the cache itself, or another array of its shape; the
+ * slots that no row names are not written).  index[r] = -1 skips the row: its y
+ * is zero.  A slot outside the cache, or one that an earlier row names too, is
+ * skipped the same way and reported: info[r] (may be NULL) is -1, or 0 (outside)
+ * or 1 (named twice).
+ */
+typedef struct {
+    int64_t dtype, flags, batch, slots, d, n, groups;
+    const void *x, *dt, *z, *B, *C;   /* z may be NULL */
+    int64_t x_row, dt_row, z_row, B_row, C_row, B_group, C_group, y_row;
+    const void *A, *D, *dt_bias;
+    const void *cache;
+    void *cache_out, *y;
+    const int32_t *index;
+    int32_t *info;
+} selinv_scan_step;
+selinv_status selinv_selective_scan_step(const selinv_scan_step *a, void *stream);
+
+/*
+ * Causal convolution of each channel, 2 <= k <= 8 taps:
+ *   y_t = bias + sum_j weight[c, j] x_{t-k+1+j},  y_t sigmoid(y_t) with SELINV_SILU,
+ * the k - 1 inputs before a sequence's first row taken from state (or zero).
+ * state_out (may be NULL; must not overlap state) gets each sequence's last
+ * k - 1 inputs, those before its first row included.  No workspace.
+ */
+typedef struct {
+    int64_t dtype, flags;             /* SELINV_SILU or 0 */
+    int64_t lines, rows, d, k;
+    int64_t sequences, live;
+    const int64_t *table;
+    selinv_view x;
+    const void *weight;               /* [d, k] */
+    const void *bias;                 /* [d] or NULL */
+    const void *state;                /* [lines or sequences, k - 1, d] or NULL */
+} selinv_conv_inputs;
+selinv_status selinv_causal_conv(const selinv_conv_inputs *a, const selinv_view *y, void *state_out, void *stream);
+
+/*
+ * Its cotangents: xb, weightb [d, k] and, where not NULL, biasb [d] (both in the
+ * arithmetic type) and stateb_out (layout of `state`); stateb is the final states' (NULL = zero).
+ */
+typedef struct {
+    selinv_view yb;
+    const void *stateb;
+    selinv_view xb;
+    void *weightb, *biasb, *stateb_out;
+} selinv_conv_grads;
+size_t selinv_causal_conv_backward_workspace_size(const selinv_conv_inputs *a);
+selinv_status selinv_causal_conv_backward(const selinv_conv_inputs *a, const selinv_conv_grads *g, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+/* The convolution for single tokens over a cache of states [slots, k - 1, d]; slots as in selinv_selective_scan_step. */
+typedef struct {
+    int64_t dtype, flags, batch, slots, d, k;
+    const void *x, *weight, *bias, *cache;
+    int64_t x_row, y_row;
+    void *cache_out, *y;
+    const int32_t *index;
+    int32_t *info;
+} selinv_conv_step;
+selinv_status selinv_causal_conv_step(const selinv_conv_step *a, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,403 @@
+// Shared pieces of the sequence operators (selective scan, causal
+// convolution): element types, pair arithmetic, exponentials, the row ranges
+// of lines and ragged sequences, and lane reductions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/selinv.h"
+#include <cstddef>
+#include <cstring>
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace selinv {
+
+// ---- element types: storage T, arithmetic C (32 bits for the 16-bit types) --
+
+template <class T> struct Elem;
+template <> struct Elem<float> {
+    using C = float;
+    SELINV_DEVINL static float up(float v) { return v; }
+    SELINV_DEVINL static float down(float v) { return v; }
+};
+template <> struct Elem<double> {
+    using C = double;
+    SELINV_DEVINL static double up(double v) { return v; }
+    SELINV_DEVINL static double down(double v) { return v; }
+};
+template <> struct Elem<__nv_bfloat16> {
+    using C = float;
+    SELINV_DEVINL static float up(__nv_bfloat16 v) { return __bfloat162float(v); }
+    SELINV_DEVINL static __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct Elem<__half> {
+    using C = float;
+    SELINV_DEVINL static float up(__half v) { return __half2float(v); }
+    SELINV_DEVINL static __half down(float v) { return __float2half_rn(v); }
+};
+
+// E consecutive elements as they lie in memory, held in 32-bit words.
+template <class T, int E> struct Pack {
+    static_assert(E * sizeof(T) % 4 == 0 && E * sizeof(T) <= 16, "4, 8 or 16 bytes");
+    static constexpr int W = E * (int)sizeof(T) / 4;
+    uint32_t w[W];
+
+    SELINV_DEVINL void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0u;
+    }
+    SELINV_DEVINL typename Elem<T>::C get(int e) const
+    {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t v = w[e >> 1];
+            const unsigned short h = (e & 1) ? (unsigned short)(v >> 16) : (unsigned short)(v & 0xffffu);
+            T t;
+            memcpy(&t, &h, 2);
+            return Elem<T>::up(t);
+        } else if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(w[e]);
+        } else {
+            return __hiloint2double((int)w[2 * e + 1], (int)w[2 * e]);
+        }
+    }
+    SELINV_DEVINL void set(const typename Elem<T>::C *v)
+    {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if constexpr (sizeof(T) == 2) {
+                const T t = Elem<T>::down(v[e]);
+                unsigned short h;
+                memcpy(&h, &t, 2);
+                if (e & 1)
+                    w[e >> 1] |= (uint32_t)h << 16;
+                else
+                    w[e >> 1] = h;
+            } else if constexpr (sizeof(T) == 4) {
+                w[e] = __float_as_uint(v[e]);
+            } else {
+                w[2 * e] = (uint32_t)__double2loint(v[e]);
+                w[2 * e + 1] = (uint32_t)__double2hiint(v[e]);
+            }
+        }
+    }
+    // The first `n` of the elements at p; `wide`: p is aligned to the whole pack.
+    SELINV_DEVINL void load(const T *p, int n, bool wide)
+    {
+        if (wide && n >= E) {
+            if constexpr (W == 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(p);
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            } else if constexpr (W == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                w[0] = v.x, w[1] = v.y;
+            } else {
+                w[0] = *reinterpret_cast<const uint32_t *>(p);
+            }
+            return;
+        }
+        clear();
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (e < n) {
+                if constexpr (sizeof(T) == 2) {
+                    const uint32_t h = reinterpret_cast<const unsigned short *>(p)[e];
+                    w[e >> 1] |= (e & 1) ? h << 16 : h;
+                } else if constexpr (sizeof(T) == 4) {
+                    w[e] = reinterpret_cast<const uint32_t *>(p)[e];
+                } else {
+                    w[2 * e] = reinterpret_cast<const uint32_t *>(p)[2 * e];
+                    w[2 * e + 1] = reinterpret_cast<const uint32_t *>(p)[2 * e + 1];
+                }
+            }
+    }
+    SELINV_DEVINL void store(T *p, int n, bool wide) const
+    {
+        if (wide && n >= E) {
+            if constexpr (W == 4)
+                *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            else if constexpr (W == 2)
+                *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint32_t *>(p) = w[0];
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (e < n) {
+                if constexpr (sizeof(T) == 2)
+                    reinterpret_cast<unsigned short *>(p)[e] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
+                else if constexpr (sizeof(T) == 4)
+                    reinterpret_cast<uint32_t *>(p)[e] = w[e];
+                else {
+                    reinterpret_cast<uint32_t *>(p)[2 * e] = w[2 * e];
+                    reinterpret_cast<uint32_t *>(p)[2 * e + 1] = w[2 * e + 1];
+                }
+            }
+    }
+};
+
+// ---- pairs: two neighbouring channels in one instruction (FFMA2) -----------
+
+template <class C> struct Two;
+template <> struct Two<float> {
+    using V = float2;
+};
+template <> struct Two<double> {
+    using V = double2;
+};
+
+SELINV_DEVINL unsigned long long bits2(float2 v)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+SELINV_DEVINL float2 from_bits2(unsigned long long r)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+SELINV_DEVINL float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return from_bits2(r);
+}
+SELINV_DEVINL float2 mul2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from_bits2(r);
+}
+SELINV_DEVINL float2 add2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from_bits2(r);
+}
+SELINV_DEVINL double2 fma2(double2 a, double2 b, double2 c)
+{
+    return make_double2(fma(a.x, b.x, c.x), fma(a.y, b.y, c.y));
+}
+SELINV_DEVINL double2 mul2(double2 a, double2 b) { return make_double2(a.x * b.x, a.y * b.y); }
+SELINV_DEVINL double2 add2(double2 a, double2 b) { return make_double2(a.x + b.x, a.y + b.y); }
+SELINV_DEVINL float2 make2(float x, float y) { return make_float2(x, y); }
+SELINV_DEVINL double2 make2(double x, double y) { return make_double2(x, y); }
+
+// ---- exponentials ----------------------------------------------------------
+
+template <class C> __host__ __device__ constexpr C log2e() { return (C)1.4426950408889634073599246810018921; }
+template <class C> __host__ __device__ constexpr C ln2() { return (C)0.69314718055994530941723212145817657; }
+
+// 2^x.  Results below the normal range become zero in float: a decay that small leaves nothing of a state.
+SELINV_DEVINL float exp2_(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+SELINV_DEVINL double exp2_(double x) { return exp2(x); }
+SELINV_DEVINL float rcp_(float x) { return __fdividef(1.0f, x); }
+SELINV_DEVINL double rcp_(double x) { return 1.0 / x; }
+
+// 1 / (1 + e^-x).
+template <class C> SELINV_DEVINL C sigmoid_(C x) { return rcp_((C)1 + exp2_(-log2e<C>() * x)); }
+SELINV_DEVINL double sigmoid_(double x) { return 1.0 / (1.0 + exp(-x)); }
+
+// d/dx of x sigmoid(x), given p = sigmoid(x).
+template <class C> SELINV_DEVINL C silu_slope(C x, C p) { return p * ((C)1 + x * ((C)1 - p)); }
+
+// log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].  In float log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
+// by atanh's odd power series cut after s^13 (the next term is under 2^-27 of the sum): relative error of a few
+// rounding steps also for far negative x, where log(1 + e) itself would lose e's low bits.
+SELINV_DEVINL float softplus_(float x)
+{
+    const float e = exp2_(-log2e<float>() * fabsf(x));
+    const float s = __fdividef(e, 2.0f + e), q = s * s;
+    float r = 1.0f / 13.0f;
+    r = fmaf(r, q, 1.0f / 11.0f);
+    r = fmaf(r, q, 1.0f / 9.0f);
+    r = fmaf(r, q, 1.0f / 7.0f);
+    r = fmaf(r, q, 1.0f / 5.0f);
+    r = fmaf(r, q, 1.0f / 3.0f);
+    r = fmaf(r * q, s, s);
+    // a NaN stays one (fmaxf alone would drop it)
+    return x == x ? fmaf(2.0f, r, fmaxf(x, 0.0f)) : x;
+}
+SELINV_DEVINL double softplus_(double x) { return x == x ? fmax(x, 0.0) + log1p(exp(-fabs(x))) : x; }
+
+// ---- reductions over lanes -------------------------------------------------
+
+template <class C> SELINV_DEVINL C shfl_xor_(C v, int m) { return __shfl_xor_sync(FULL_MASK, v, m); }
+
+// Sums of V values over the lanes that differ in the bits [LO, HI) of the lane number (powers of two); the values
+// are dealt out over those lanes as they are summed, so that a lane ends with max(1, V * LO / HI) of them, in v[0..]:
+// those from scatter_first() on.  With more lanes than values, lanes that differ in the lowest bits hold the same.
+template <int V, int LO, int HI, class C> SELINV_DEVINL void scatter_sum(C *v, int lane)
+{
+    if constexpr (HI > LO) {
+        constexpr int B = HI / 2;
+        if constexpr (V > 1) {
+            const bool up = lane & B;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const C send = up ? v[i] : v[i + V / 2], keep = up ? v[i + V / 2] : v[i];
+                v[i] = keep + shfl_xor_(send, B);
+            }
+            scatter_sum<V / 2, LO, B>(v, lane);
+        } else {
+            v[0] += shfl_xor_(v[0], B);
+            scatter_sum<1, LO, B>(v, lane);
+        }
+    }
+}
+template <int V, int LO, int HI> SELINV_DEVINL int scatter_first(int lane)
+{
+    if constexpr (HI > LO && V > 1)
+        return ((lane & (HI / 2)) ? V / 2 : 0) + scatter_first<V / 2, LO, HI / 2>(lane);
+    else
+        return 0;
+}
+// Whether this lane is the one of its equals that writes.
+template <int V, int LO, int HI> SELINV_DEVINL bool scatter_writes(int lane)
+{
+    if constexpr (HI > LO && V > 1)
+        return scatter_writes<V / 2, LO, HI / 2>(lane);
+    else if constexpr (HI > LO)
+        return (lane & (HI - LO)) == 0;
+    else
+        return true;
+}
+
+// ---- rows ------------------------------------------------------------------
+//
+// A call covers `lines` lines of `rows` rows.  Without a table every line is
+// one sequence.  With one there is a single line, cut into sequences: the
+// table (device memory, int64) holds the first rows of the `live` sequences
+// that have any, ascending, then `rows`, then those sequences' numbers.
+
+struct Rows {
+    const int64_t *table;
+    int64_t live, rows;
+    // The live sequence that row r lies in (r < rows).
+    SELINV_DEVINL int64_t find(int64_t r) const
+    {
+        if (!table) return 0;
+        int64_t lo = 0, hi = live;
+        while (hi - lo > 1) {
+            const int64_t m = (lo + hi) / 2;
+            if (table[m] <= r)
+                lo = m;
+            else
+                hi = m;
+        }
+        return lo;
+    }
+    SELINV_DEVINL int64_t start(int64_t k) const { return table ? table[k] : 0; }
+    SELINV_DEVINL int64_t end(int64_t k) const { return table ? table[k + 1] : rows; }
+    SELINV_DEVINL int64_t number(int64_t k, int64_t line) const { return table ? table[live + 1 + k] : line; }
+    // Which of the rows r0 .. r0 + n (n <= 31, one more than the n asked for) begin a sequence, given that row r0 lies
+    // in the live sequence k; `rows` itself counts as one.  Every lane of the warp calls it.
+    SELINV_DEVINL uint32_t starts(int64_t r0, int n, int64_t k, int lane) const
+    {
+        if (!table) return (r0 == 0 ? 1u : 0u) | (r0 + n >= rows ? 1u << (int)(rows - r0) : 0u);
+        uint32_t bit = 0;
+        if (k + lane <= live) {
+            const int64_t at = table[k + lane] - r0;
+            if (at >= 0 && at <= n) bit = 1u << (int)at;
+        }
+        return __reduce_or_sync(FULL_MASK, bit);
+    }
+};
+
+// An array [lines, rows, channels]: strides in elements, channels contiguous.  `wide`: base, strides and the first
+// channel of every group lie on 16 bytes, so that packs may be moved whole.
+template <class P> struct Strided {
+    P p;
+    int64_t line, row;
+    bool wide;
+};
+using In = Strided<const void *>;
+using Out = Strided<void *>;
+
+struct ScanArgs {
+    Rows rows;
+    int64_t lines, d, sequences;
+    int n, groups;
+    bool softplus;
+    In x, dt, z, B, C;          // z.p may be null
+    int64_t B_group, C_group;
+    const void *A, *D, *dt_bias, *state;     // D, dt_bias, state may be null
+    Out y;
+    void *state_out, *kept;     // may be null
+    // lines cut into segments of seg_rows rows: the state each leaves behind from zero, and the sum of its steps
+    int segs;
+    int64_t seg_rows;
+    void *ends, *sums;
+};
+
+struct ScanGrads {
+    const void *kept;
+    In yb;
+    const void *stateb;         // cotangent of the final states, or null
+    Out xb, dtb, zb, Bb, Cb;    // zb.p may be null
+    int64_t Bb_group, Cb_group;
+    void *Ab, *Db, *dt_biasb, *stateb_out;   // the last three may be null
+    // partial sums: of B and C over the channels of a block, of the parameters over a segment
+    void *part_bc, *part_a, *part_d, *part_bias;
+};
+
+struct ScanStepArgs {
+    int64_t batch, d, slots;
+    int n, groups;
+    bool softplus;
+    const void *x, *dt, *z, *B, *C;
+    int64_t x_row, dt_row, z_row, B_row, C_row, B_group, C_group, y_row;
+    const void *A, *D, *dt_bias;
+    const void *cache;
+    void *cache_out, *y;
+    const int32_t *index;
+    int32_t *info;
+};
+
+struct ConvArgs {
+    Rows rows;
+    int64_t lines, d, sequences;
+    int k;
+    bool silu;
+    In x;
+    const void *weight, *bias, *state;
+    Out y;
+    void *state_out;
+    // backward
+    In yb;
+    const void *stateb;
+    Out xb;
+    void *weightb, *biasb, *stateb_out;
+    void *part;
+    int64_t chunk_rows;
+    int chunks;
+};
+
+struct ConvStepArgs {
+    int64_t batch, d, slots;
+    int k;
+    bool silu;
+    const void *x, *weight, *bias, *cache;
+    int64_t x_row, y_row;
+    void *cache_out, *y;
+    const int32_t *index;
+    int32_t *info;
+};
+
+// Status of a row of a step (info): done, its slot lies outside the cache, or an earlier row names the same slot.
+constexpr int32_t STEP_OK = -1, STEP_RANGE = 0, STEP_TWICE = 1;
+
+}  // namespace selinv

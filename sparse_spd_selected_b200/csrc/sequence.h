@@ -1,0 +1,23 @@
+// Launchers of the sequence operators, one set per element type.
+#pragma once
+
+#include "sequence.cuh"
+
+namespace selinv {
+
+// The warp tiles of the scan: states padded to NP = 4, 8, 16, 32 or 64; `narrow` tiles hold a quarter of the
+// channels (float64 has these only, and the backward where a wide one's states do not fit).
+template <class T> int scan_tile_channels(int n, bool narrow, bool backward);
+template <class T> cudaError_t scan_launch(const ScanArgs &p, bool narrow, cudaStream_t s);
+template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, bool narrow, cudaStream_t s);
+template <class T> cudaError_t scan_step_launch(const ScanStepArgs &p, cudaStream_t s);
+template <class T> cudaError_t conv_launch(const ConvArgs &p, cudaStream_t s);
+template <class T> cudaError_t conv_backward_launch(const ConvArgs &p, cudaStream_t s);
+template <class T> cudaError_t conv_step_launch(const ConvStepArgs &p, cudaStream_t s);
+
+constexpr int SCAN_MAX_N = 64, CONV_MIN_K = 2, CONV_MAX_K = 8;
+constexpr int scan_padded(int n) { return n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64; }
+constexpr int SCAN_KEEP_ROWS = 16;      // rows between the states kept for the backward
+constexpr int SCAN_BLOCK_TILES = 4;     // warp tiles of a block
+
+}  // namespace selinv

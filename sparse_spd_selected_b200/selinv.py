@@ -14,7 +14,9 @@ inverse), plus log det A and A^-1 r from the same factorisation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -57,6 +59,16 @@ class NonFiniteInputError(SelinvError):
         self.info = info
         blocks = [(-3 - v) if v <= -3 else None for v in info]
         super().__init__(ERR_INVALID_ARG, f"first block with a non-finite entry per batch element: {blocks}")
+
+
+class SlotError(SelinvError):
+    """A step's index names a slot outside the cache, or one slot twice."""
+
+    def __init__(self, info):
+        self.info = info
+        what = {0: "outside the cache", 1: "named by an earlier row too"}
+        rows = {r: what.get(v, v) for r, v in enumerate(info) if v != -1}
+        super().__init__(ERR_INVALID_ARG, f"slots of rows {rows}")
 
 
 class SingularBlockError(SelinvError):
@@ -136,6 +148,18 @@ def lib():
         L.selinv_tree_sample.argtypes = [P, ctypes.c_int, I32, P, P, P, P, P, P, P, SZ, P]
         L.selinv_tree_sample.restype = ctypes.c_int
         L.selinv_tree.restype = ctypes.c_int
+        S = ctypes.c_char_p                                  # a packed struct of the sequence operators
+        for name, args in (("selinv_selective_scan_kept_size", [S]), ("selinv_selective_scan_workspace_size", [S]),
+                           ("selinv_selective_scan_backward_workspace_size", [S]),
+                           ("selinv_causal_conv_backward_workspace_size", [S])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = SZ
+        for name, args in (("selinv_selective_scan", [S, S, P, P, P, SZ, P]),
+                           ("selinv_selective_scan_backward", [S, S, P, SZ, P]),
+                           ("selinv_selective_scan_step", [S, P]), ("selinv_causal_conv", [S, S, P, P]),
+                           ("selinv_causal_conv_backward", [S, S, P, SZ, P]), ("selinv_causal_conv_step", [S, P])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -942,3 +966,506 @@ def tree_sample(plan: TreePlan, diag: torch.Tensor, edge: torch.Tensor, z: torch
     _check(st, "selinv_tree_sample")
     _raise_on_info(info, check)
     return {"eta": eta[0] if single else eta, "logdet": logdet, "info": info}
+
+
+# ---- sequence operators: selective scan and causal convolution -------------
+#
+# The state-space layer along chains.  The selective scan is the solve of a
+# block lower-bidiagonal system -- the matrices whose selected inverse bidiag
+# gives -- with M_tt = I and M_{t,t-1} = -diag(exp(dt_t A)), read out by C; the
+# causal convolution stands in front of it.
+
+BF16, F16 = 2, 3
+_ELEMENTS = {torch.float64: F64, torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+_SOFTPLUS, _SILU = 1, 2
+_SCAN_INPUTS = struct.Struct("9qP" + "Pqq" * 5 + "qq" + "4P")
+_SCAN_GRADS = struct.Struct("P" + "Pqq" + "P" + "Pqq" * 5 + "qq" + "4P")
+_SCAN_STEP = struct.Struct("7q5P8q3PPPPPP")
+_CONV_INPUTS = struct.Struct("8qP" + "Pqq" + "3P")
+_CONV_GRADS = struct.Struct("Pqq" + "P" + "Pqq" + "3P")
+_CONV_STEP = struct.Struct("6q4P2qPPPP")
+_VIEW = struct.Struct("Pqq")
+
+
+def _arith(dtype):
+    """The type of sums, states and parameters."""
+    return torch.float64 if dtype == torch.float64 else torch.float32
+
+
+def _element_code(name, t) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = _ELEMENTS.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float64, float32, bfloat16 or float16, not {t.dtype}")
+    return code
+
+
+def _like(name, t, dtype, device, shape, contiguous=True):
+    """Checks a tensor's type, device and shape; returns its address (0 for None)."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _view(name, t, inner, output=False):
+    """(address, stride between lines, stride between rows) of a tensor [..., rows, *inner dims]: its last dimension
+    contiguous, its leading dimensions one even stride apart."""
+    if t.numel() == 0:
+        return t.data_ptr(), 0, 0
+    st, sh = t.stride(), t.shape
+    at = len(sh) - 1 - inner
+    if st[-1] != 1 and sh[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    line = 0
+    for i in range(at - 1, -1, -1):
+        if sh[i] == 1:
+            continue
+        if line == 0:
+            line, size = st[i], sh[i]
+        elif st[i] == line * size:
+            size *= sh[i]
+        else:
+            raise ValueError(f"{name}'s leading dimensions must be evenly strided")
+    if output and t.numel() > 0:
+        need = 1
+        for size, stride in sorted(((n, v) for n, v in zip(sh, st) if n > 1), key=lambda e: e[1]):
+            if stride < need:
+                raise ValueError(f"{name} must not overlap itself")
+            need = size * stride
+    return t.data_ptr(), line, st[at]
+
+
+def _span(t):
+    """First and last byte of a tensor."""
+    if t.numel() == 0:
+        return 0, 0
+    n = sum((size - 1) * stride for size, stride in zip(t.shape, t.stride())) + 1
+    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+
+def _apart(name, t, others):
+    """Refuses an output that shares memory with an input.  Two slices of the channels of one array (equal strides)
+    are told apart; anything else that may overlap is refused."""
+    a0, a1 = _span(t)
+    for other, u in others:
+        if u is None or u.device != t.device:
+            continue
+        b0, b1 = _span(u)
+        if a1 <= b0 or b1 <= a0:
+            continue
+        if t.dtype == u.dtype and t.dim() == u.dim() and t.dim() > 1 and t.stride() == u.stride() and t.stride(-1) == 1:
+            row = min(s for s, n in zip(t.stride()[:-1], t.shape[:-1]) if n > 1) if t.numel() > t.shape[-1] else 0
+            gap = abs(a0 - b0) // t.element_size()
+            if row:
+                gap %= row
+                lo, hi = (t, u) if (a0 < b0) else (u, t)
+                if lo.shape[-1] <= gap and gap + hi.shape[-1] <= row:
+                    continue
+        raise ValueError(f"{name} must not overlap {other}")
+
+
+def _placed(first):
+    """Runs a call on its first tensor's device, on `stream` where one is given: what it allocates belongs there too."""
+    def wrap(fn):
+        @functools.wraps(fn)
+        def call(*args, stream=None, **kw):
+            t = args[0] if args else kw.get(first)
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise ValueError(f"{first} must be a CUDA tensor")
+            if stream is None and t.device.index == torch._C._cuda_getDevice():
+                return fn(*args, **kw)
+            if stream is not None and stream.device != t.device:
+                raise ValueError(f"stream belongs to {stream.device}, {first} to {t.device}")
+            with torch.cuda.device(t.device), torch.cuda.stream(stream):
+                return fn(*args, **kw)
+        return call
+    return wrap
+
+
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+class SequencePlan:
+    """Sequences of the given lengths (0 and more) one after another in one array of rows; the table that the kernels
+    read is cached on the device.  A call may pass arrays with more rows than the plan's: those behind the last
+    sequence are neither read nor written (zero in outputs that the call allocates)."""
+
+    def __init__(self, lengths, device=None):
+        lengths = [int(n) for n in lengths]
+        if any(n < 0 for n in lengths):
+            raise ValueError("lengths must not be negative")
+        self.lengths = lengths
+        self.sequences = len(lengths)
+        first, live, empty, at = [], [], [], 0
+        for i, n in enumerate(lengths):
+            if n:
+                first.append(at)
+                live.append(i)
+                at += n
+            else:
+                empty.append(i)
+        self.rows, self.live = at, len(live)
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.table = torch.tensor(first + [at] + live + empty, dtype=torch.int64, device=device)
+
+
+def _rows_of(name, x, plan, inner=1):
+    """(lines, rows, sequences, live, table address, leading shape, number of states) of x [..., rows, d]."""
+    if x.dim() < 1 + inner:
+        raise ValueError(f"{name} must be [..., rows, d]")
+    lead = x.shape[:-1 - inner]
+    rows = x.shape[-1 - inner]
+    if plan is None:
+        lines = 1
+        for n in lead:
+            lines *= n
+        return lines, rows, 0, 0, 0, tuple(lead)
+    if lead:
+        raise ValueError(f"with a plan {name} must be [rows, d]")
+    if plan.rows > rows:
+        raise ValueError(f"the plan has {plan.rows} rows, {name} {rows}")
+    if plan.table.device != x.device:
+        raise ValueError(f"the plan is on {plan.table.device}, {name} on {x.device}")
+    return 1, plan.rows, plan.sequences, plan.live, plan.table.data_ptr(), (plan.sequences,)
+
+
+def _output(out, key, shape, dtype, device, plan, inputs):
+    """out[key], checked, or a new tensor; rows behind a plan's are zero in a new one and left alone in a given one."""
+    t = out.get(key) if out else None
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        if plan is not None and shape[0] > plan.rows:
+            t[plan.rows:].zero_()
+        return t
+    _like(f"out[{key!r}]", t, dtype, device, shape, contiguous=False)
+    _apart(f"out[{key!r}]", t, inputs)
+    return t
+
+
+def _dense_output(out, key, shape, dtype, device, inputs):
+    t = out.get(key) if out else None
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _like(f"out[{key!r}]", t, dtype, device, shape)
+    _apart(f"out[{key!r}]", t, inputs)
+    return t
+
+
+def _conv_inputs(x, weight, bias, silu, state, plan):
+    code, dt, dev = _element_code("x", x), x.dtype, x.device
+    lines, rows, sequences, live, table, lead = _rows_of("x", x, plan)
+    d = x.shape[-1]
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [d, k]")
+    k = weight.shape[1]
+    states = lead + (k - 1, d)
+    packed = _CONV_INPUTS.pack(code, _SILU if silu else 0, lines, rows, d, k, sequences, live, table, *_view("x", x, 1),
+                               _like("weight", weight, dt, dev, (d, k)), _like("bias", bias, dt, dev, (d,)),
+                               _like("state", state, dt, dev, states))
+    return packed, states, d, k
+
+
+@_placed("x")
+def causal_conv(x, weight, bias=None, *, silu=False, state=None, plan=None, want_state=True, out=None):
+    """Causal convolution of each channel: y_t = bias + sum_j weight[:, j] x_{t-k+1+j}, then silu where asked.
+
+    x [..., rows, d] (channels contiguous, any strides between rows; with a
+    SequencePlan [rows, d], the sequences one after another), weight [d, k]
+    with 2 <= k <= 8, bias [d], all float64, float32, bfloat16 or float16;
+    state [..., k-1, d] (with a plan [sequences, k-1, d]): the inputs before
+    the first row, zero when None.  Returns a dict with y and, if want_state,
+    state: the last k-1 inputs of each sequence, from which the next call or
+    causal_conv_step goes on.  ``out`` may hold preallocated y and state (not
+    overlapping the inputs)."""
+    packed, states, d, k = _conv_inputs(x, weight, bias, silu, state, plan)
+    given = (("x", x), ("weight", weight), ("bias", bias), ("state", state)) if out else ()
+    y = _output(out, "y", x.shape, x.dtype, x.device, plan, given)
+    new = _dense_output(out, "state", states, x.dtype, x.device, given) if want_state else None
+    _check(lib().selinv_causal_conv(packed, _VIEW.pack(*_view("y", y, 1, out is not None)),
+                                    0 if new is None else new.data_ptr(), _raw_stream(x.device)), "selinv_causal_conv")
+    return {"y": y, "state": new}
+
+
+@_placed("x")
+def causal_conv_backward(x, weight, yb, *, bias=None, stateb=None, silu=False, state=None, plan=None, out=None,
+                         workspace=None):
+    """Cotangents of causal_conv from those of y (yb, x's shape) and of the final states (stateb, None = zero).
+    Returns a dict with xb, weightb [d, k] and biasb [d] (float32; float64 for float64), and stateb (the initial
+    states'; None without state)."""
+    packed, states, d, k = _conv_inputs(x, weight, bias, silu, state, plan)
+    dt, dev, ct = x.dtype, x.device, _arith(x.dtype)
+    _like("yb", yb, dt, dev, x.shape, contiguous=False)
+    given = (("x", x), ("weight", weight), ("bias", bias), ("state", state), ("yb", yb), ("stateb", stateb)) if out else ()
+    xb = _output(out, "xb", x.shape, dt, dev, plan, given)
+    weightb = _dense_output(out, "weightb", (d, k), ct, dev, given)
+    biasb = _dense_output(out, "biasb", (d,), ct, dev, given)
+    new = _dense_output(out, "stateb", states, dt, dev, given) if state is not None else None
+    L = lib()
+    nbytes = L.selinv_causal_conv_backward_workspace_size(packed)
+    ws = _workspace(nbytes, dev, workspace)
+    grads = _CONV_GRADS.pack(*_view("yb", yb, 1), _like("stateb", stateb, dt, dev, states),
+                             *_view("xb", xb, 1, out is not None), weightb.data_ptr(), biasb.data_ptr(),
+                             0 if new is None else new.data_ptr())
+    _check(L.selinv_causal_conv_backward(packed, grads, 0 if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev)),
+           "selinv_causal_conv_backward")
+    return {"xb": xb, "weightb": weightb, "biasb": biasb, "stateb": new}
+
+
+class _CausalConvFn(torch.autograd.Function):
+    """y, state = causal_conv(...) with its analytic backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, state, silu, plan):
+        r = causal_conv(x, weight, bias, silu=silu, state=state, plan=plan)
+        ctx.silu, ctx.plan = silu, plan
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, weight, bias, state)
+        return r["y"], r["state"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, yb, stateb):
+        x, weight, bias, state = ctx.saved_tensors
+        yb = torch.zeros_like(x, memory_format=torch.contiguous_format) if yb is None else _view_or_copy(yb)
+        r = causal_conv_backward(x, weight, yb, bias=bias, stateb=None if stateb is None else stateb.contiguous(),
+                                 silu=ctx.silu, state=state, plan=ctx.plan)
+        return (r["xb"], r["weightb"].to(weight.dtype), None if bias is None else r["biasb"].to(bias.dtype), r["stateb"],
+                None, None)
+
+
+def _view_or_copy(t):
+    """t itself where the kernels can read it as it lies, else a contiguous copy."""
+    try:
+        _view("yb", t, 1)
+        return t
+    except ValueError:
+        return t.contiguous()
+
+
+def causal_conv_ad(x, weight, bias=None, *, silu=False, state=None, plan=None):
+    """Differentiable causal_conv: returns (y, state); gradients reach x, weight, bias and state through
+    causal_conv_backward."""
+    return _CausalConvFn.apply(x, weight, bias, state, silu, plan)
+
+
+def _step_slots(cache, shape, batch, index, cache_out, check, dev):
+    """(slots, cache_out, index address, info) of a step over cache [slots, *shape]."""
+    if cache.dim() != 1 + len(shape):
+        raise ValueError(f"cache must be [slots, {', '.join(str(n) for n in shape)}]")
+    slots = cache.shape[0]
+    if cache_out is None:
+        cache_out = cache
+    elif cache_out.data_ptr() != cache.data_ptr() or cache_out.shape != cache.shape:
+        _apart("cache_out", cache_out, (("cache", cache),))
+    info = None
+    if index is None:
+        if slots < batch:
+            raise ValueError(f"{batch} rows need as many slots, the cache has {slots}")
+        return slots, cache_out, 0, None
+    at = _like("index", index, torch.int32, dev, (batch,))
+    if check:
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("check=True reads the slots' status back: pass check=False in a captured call")
+        info = torch.empty(batch, dtype=torch.int32, device=dev)
+    return slots, cache_out, at, info
+
+
+def _raise_on_slots(info):
+    if info is not None:
+        host = info.cpu()
+        if bool((host != -1).any()):
+            raise SlotError(host.tolist())
+
+
+@_placed("cache")
+def causal_conv_step(cache, x, weight, bias=None, *, silu=False, index=None, cache_out=None, check=True, out=None):
+    """causal_conv for single tokens: row r of x [batch, d] continues slot index[r] (int32; None: slot r) of cache
+    [slots, k-1, d], which is moved on in place, or into the same slots of cache_out.  index[r] = -1 skips the row (its
+    y is zero).  A slot outside the cache, or one that an earlier row names, is skipped too; with check=True the call
+    synchronises once and raises SlotError for it.  Returns y [batch, d]."""
+    code, dt, dev = _element_code("x", x), x.dtype, x.device
+    if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("x must be [batch, d] and weight [d, k]")
+    (batch, d), k = x.shape, weight.shape[1]
+    slots, new, at, info = _step_slots(cache, (k - 1, d), batch, index, cache_out, check, dev)
+    given = (("x", x), ("weight", weight), ("bias", bias), ("cache", cache), ("cache_out", new)) if out else ()
+    y = _output(out, "y", (batch, d), dt, dev, None, given)
+    xp, _, x_row = _view("x", x, 1)
+    yp, _, y_row = _view("y", y, 1, out is not None)
+    packed = _CONV_STEP.pack(code, _SILU if silu else 0, batch, slots, d, k, xp, _like("weight", weight, dt, dev, (d, k)),
+                             _like("bias", bias, dt, dev, (d,)), _like("cache", cache, dt, dev, (slots, k - 1, d)),
+                             x_row, y_row, _like("cache_out", new, dt, dev, (slots, k - 1, d)), yp, at,
+                             0 if info is None else info.data_ptr())
+    _check(lib().selinv_causal_conv_step(packed, _raw_stream(dev)), "selinv_causal_conv_step")
+    _raise_on_slots(info)
+    return y
+
+
+def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, state, plan):
+    code, ty, dev, ct = _element_code("x", x), x.dtype, x.device, _arith(x.dtype)
+    lines, rows, sequences, live, table, lead = _rows_of("x", x, plan)
+    d = x.shape[-1]
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be [d, n]")
+    n = A.shape[1]
+    _like("dt", dt, ty, dev, x.shape, False)
+    _like("z", z, ty, dev, x.shape, False)
+    if not isinstance(B, torch.Tensor) or B.dim() != x.dim() + 1:
+        raise ValueError("B must be [..., rows, groups, n]")
+    groups = B.shape[-2]
+    bc = x.shape[:-1] + (groups, n)
+    _like("B", B, ty, dev, bc, False)
+    _like("C", C, ty, dev, bc, False)
+    if groups < 1 or d % groups:
+        raise ValueError(f"{d} channels do not divide into {groups} groups")
+    states = lead + (d, n)
+    packed = _SCAN_INPUTS.pack(code, _SOFTPLUS if softplus else 0, lines, rows, d, n, groups, sequences, live, table,
+                               *_view("x", x, 1), *_view("dt", dt, 1), *((0, 0, 0) if z is None else _view("z", z, 1)),
+                               *_view("B", B, 2), *_view("C", C, 2), B.stride(-2), C.stride(-2),
+                               _like("A", A, ct, dev, (d, n)), _like("D", D, ct, dev, (d,)),
+                               _like("dt_bias", dt_bias, ct, dev, (d,)), _like("state", state, ct, dev, states))
+    return packed, states, d, n, groups, bc
+
+
+def _scan_given(x, dt, A, B, C, D, z, dt_bias, state, *more):
+    return (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("z", z), ("dt_bias", dt_bias),
+            ("state", state)) + more
+
+
+@_placed("x")
+def selective_scan(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=False, state=None, plan=None, keep=False,
+                   want_state=True, out=None, workspace=None):
+    """Selective state-space scan along chains:
+
+        dt' = dt + dt_bias (its softplus, if asked),  h_t = exp(dt'_t A) h_{t-1} + dt'_t x_t B_t,
+        y_t = (sum_n C_t h_t + D x_t) * silu(z_t).
+
+    x, dt, z [..., rows, d] and B, C [..., rows, groups, n] (channel c reads
+    group c // (d // groups); last dimension contiguous, any strides between
+    rows) in float64, float32, bfloat16 or float16; A [d, n], n <= 64, D and
+    dt_bias [d] and state [..., d, n] (the states before the first row, zero
+    when None) in float32 (float64 for float64).  With a SequencePlan x is
+    [rows, d], the sequences one after another, and state [sequences, d, n].
+    Returns a dict with y, state (the final states, if want_state) and kept
+    (what selective_scan_backward needs, if keep).  ``out`` may hold
+    preallocated y and state (not overlapping the inputs)."""
+    packed, states, d, n, groups, _ = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, state, plan)
+    dev, ct = x.device, _arith(x.dtype)
+    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state) if out else ()
+    y = _output(out, "y", x.shape, x.dtype, dev, plan, given)
+    new = _dense_output(out, "state", states, ct, dev, given) if want_state else None
+    L = lib()
+    kept = None
+    if keep:
+        kept = torch.empty(L.selinv_selective_scan_kept_size(packed) // ct.itemsize, dtype=ct, device=dev)
+    nbytes = L.selinv_selective_scan_workspace_size(packed)
+    ws = _workspace(nbytes, dev, workspace)
+    _check(L.selinv_selective_scan(packed, _VIEW.pack(*_view("y", y, 1, out is not None)),
+                                   0 if new is None else new.data_ptr(), 0 if kept is None else kept.data_ptr(),
+                                   0 if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev)), "selinv_selective_scan")
+    return {"y": y, "state": new, "kept": kept}
+
+
+@_placed("kept")
+def selective_scan_backward(kept, x, dt, A, B, C, yb, *, D=None, stateb=None, z=None, dt_bias=None, softplus=False,
+                            state=None, plan=None, out=None, workspace=None):
+    """Cotangents of selective_scan from those of y (yb, x's shape) and of the final states (stateb, None = zero), on
+    the forward's inputs and its `kept`.  Returns a dict with xb, dtb, Bb, Cb, zb (None without z) in the inputs' type,
+    and Ab, Db, dt_biasb, stateb (each None without its input) in float32 (float64 for float64)."""
+    packed, states, d, n, groups, bc = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, state, plan)
+    ty, dev, ct = x.dtype, x.device, _arith(x.dtype)
+    L = lib()
+    _like("kept", kept, ct, dev, (L.selinv_selective_scan_kept_size(packed) // ct.itemsize,))
+    _like("yb", yb, ty, dev, x.shape, False)
+    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state, ("kept", kept), ("yb", yb), ("stateb", stateb)) if out else ()
+    new = {k: _output(out, k, s, ty, dev, plan, given) for k, s in (("xb", x.shape), ("dtb", x.shape), ("Bb", bc), ("Cb", bc))}
+    new["zb"] = _output(out, "zb", x.shape, ty, dev, plan, given) if z is not None else None
+    for key, ref, shape in (("Ab", A, (d, n)), ("Db", D, (d,)), ("dt_biasb", dt_bias, (d,)), ("stateb", state, states)):
+        new[key] = _dense_output(out, key, shape, ct, dev, given) if ref is not None else None
+    nbytes = L.selinv_selective_scan_backward_workspace_size(packed)
+    ws = _workspace(nbytes, dev, workspace)
+    own = out is not None
+    Bb, Cb, zb = new["Bb"], new["Cb"], new["zb"]
+    grads = _SCAN_GRADS.pack(kept.data_ptr(), *_view("yb", yb, 1), _like("stateb", stateb, ct, dev, states),
+                             *_view("xb", new["xb"], 1, own), *_view("dtb", new["dtb"], 1, own),
+                             *((0, 0, 0) if zb is None else _view("zb", zb, 1, own)), *_view("Bb", Bb, 2, own),
+                             *_view("Cb", Cb, 2, own), Bb.stride(-2), Cb.stride(-2),
+                             *(0 if new[k] is None else new[k].data_ptr() for k in ("Ab", "Db", "dt_biasb", "stateb")))
+    _check(L.selinv_selective_scan_backward(packed, grads, 0 if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev)),
+           "selinv_selective_scan_backward")
+    return new
+
+
+class _SelectiveScanFn(torch.autograd.Function):
+    """y, state = selective_scan(...) with its analytic backward."""
+
+    @staticmethod
+    def forward(ctx, x, dt, A, B, C, D, z, dt_bias, state, softplus, plan):
+        r = selective_scan(x, dt, A, B, C, D, z=z, dt_bias=dt_bias, softplus=softplus, state=state, plan=plan,
+                           keep=any(ctx.needs_input_grad))
+        ctx.softplus, ctx.plan = softplus, plan
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, state, r["kept"])
+        return r["y"], r["state"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, yb, stateb):
+        x, dt, A, B, C, D, z, dt_bias, state, kept = ctx.saved_tensors
+        yb = torch.zeros_like(x, memory_format=torch.contiguous_format) if yb is None else _view_or_copy(yb)
+        r = selective_scan_backward(kept, x, dt, A, B, C, yb, D=D, stateb=None if stateb is None else stateb.contiguous(),
+                                    z=z, dt_bias=dt_bias, softplus=ctx.softplus, state=state, plan=ctx.plan)
+        return (r["xb"], r["dtb"], r["Ab"], r["Bb"], r["Cb"], r["Db"], r["zb"], r["dt_biasb"], r["stateb"], None, None)
+
+
+def selective_scan_ad(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=False, state=None, plan=None):
+    """Differentiable selective_scan: returns (y, state); gradients reach every tensor through
+    selective_scan_backward."""
+    return _SelectiveScanFn.apply(x, dt, A, B, C, D, z, dt_bias, state, softplus, plan)
+
+
+@_placed("cache")
+def selective_scan_step(cache, x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=False, index=None,
+                        cache_out=None, check=True, out=None):
+    """selective_scan for single tokens: row r of x, dt, z [batch, d] and B, C [batch, groups, n] continues slot
+    index[r] (int32; None: slot r) of cache [slots, d, n], in place or into the same slots of cache_out.  index[r] = -1
+    skips the row (its y is zero).  A slot outside the cache, or one that an earlier row names, is skipped too; with
+    check=True the call synchronises once and raises SlotError for it.  Returns y [batch, d]."""
+    code, ty, dev, ct = _element_code("x", x), x.dtype, x.device, _arith(x.dtype)
+    if x.dim() != 2 or not isinstance(A, torch.Tensor) or A.dim() != 2 or not isinstance(B, torch.Tensor) or B.dim() != 3:
+        raise ValueError("x must be [batch, d], A [d, n] and B [batch, groups, n]")
+    (batch, d), n, groups = x.shape, A.shape[1], B.shape[1]
+    if groups < 1 or d % groups:
+        raise ValueError(f"{d} channels do not divide into {groups} groups")
+    bc = (batch, groups, n)
+    _like("dt", dt, ty, dev, x.shape, False)
+    _like("z", z, ty, dev, x.shape, False)
+    _like("B", B, ty, dev, bc, False)
+    _like("C", C, ty, dev, bc, False)
+    slots, new, at, info = _step_slots(cache, (d, n), batch, index, cache_out, check, dev)
+    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, cache, ("cache_out", new)) if out else ()
+    y = _output(out, "y", (batch, d), ty, dev, None, given)
+    xp, _, x_row = _view("x", x, 1)
+    dp, _, d_row = _view("dt", dt, 1)
+    zp, _, z_row = (0, 0, 0) if z is None else _view("z", z, 1)
+    bp, _, b_row = _view("B", B, 2)
+    cp, _, c_row = _view("C", C, 2)
+    yp, _, y_row = _view("y", y, 1, out is not None)
+    packed = _SCAN_STEP.pack(code, _SOFTPLUS if softplus else 0, batch, slots, d, n, groups, xp, dp, zp, bp, cp,
+                             x_row, d_row, z_row, b_row, c_row, B.stride(1), C.stride(1), y_row,
+                             _like("A", A, ct, dev, (d, n)), _like("D", D, ct, dev, (d,)),
+                             _like("dt_bias", dt_bias, ct, dev, (d,)), _like("cache", cache, ct, dev, (slots, d, n)),
+                             _like("cache_out", new, ct, dev, (slots, d, n)), yp, at, 0 if info is None else info.data_ptr())
+    _check(lib().selinv_selective_scan_step(packed, _raw_stream(dev)), "selinv_selective_scan_step")
+    _raise_on_slots(info)
+    return y
