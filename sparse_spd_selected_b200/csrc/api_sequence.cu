@@ -90,25 +90,25 @@ selinv_status scan_check(const selinv_scan_inputs &a)
     return SELINV_OK;
 }
 
+// Channels of a warp's tile.
+int64_t tile_channels(const selinv_scan_inputs &a, int narrow)
+{
+    return with_type(a.dtype, [&](auto t) { return scan_tile_channels<decltype(t)>((int)a.n, narrow); });
+}
+
 // How a scan is spread over the GPU.
 struct Spread {
-    bool narrow;
-    int segs;
+    int narrow, segs;
     int64_t seg_rows;
 };
 Spread scan_spread(const selinv_scan_inputs &a, bool backward)
 {
     const int64_t per = a.d / a.groups, want = 4 * (int64_t)sm_count();
-    const auto warps = [&](bool narrow) {
-        const int cw = with_type(a.dtype, [&](auto t) { return scan_tile_channels<decltype(t)>((int)a.n, narrow, backward); });
-        return a.lines * a.groups * div_up(per, cw);
-    };
-    Spread s{false, 1, a.rows};
-    if (warps(false) >= want) return s;
-    s.narrow = true;
-    const int64_t w = warps(true);
+    const auto warps = [&](int narrow) { return a.lines * a.groups * div_up(per, tile_channels(a, narrow)); };
+    Spread s{0, 1, a.rows};
+    const int64_t w = warps(s.narrow), most = a.rows / 64 > 1 ? a.rows / 64 : 1;
     if (w < want) {
-        const int64_t most = a.rows / 64 > 1 ? a.rows / 64 : 1, segs = div_up(2 * want, w);
+        const int64_t segs = div_up(2 * want, w);
         s.segs = (int)(segs < most ? segs : most);
     }
     s.seg_rows = div_up(div_up(a.rows, s.segs), SCAN_KEEP_ROWS) * SCAN_KEEP_ROWS;
@@ -137,8 +137,7 @@ ScanSpace scan_space(const selinv_scan_inputs &a, const Spread &s, bool backward
         w.sums = take(pieces * a.d * cs);
     }
     if (backward) {
-        const int cw = with_type(a.dtype, [&](auto t) { return scan_tile_channels<decltype(t)>((int)a.n, s.narrow, true); });
-        const size_t parts = div_up(div_up(a.d / a.groups, cw), SCAN_BLOCK_TILES);
+        const size_t parts = div_up(div_up(a.d / a.groups, tile_channels(a, 0)), SCAN_BLOCK_TILES);
         w.bc = take(parts * a.lines * a.rows * a.groups * 2 * scan_padded((int)a.n) * cs);
         w.a = take(pieces * a.d * a.n * cs);
         w.d = take(pieces * a.d * cs);
@@ -156,12 +155,12 @@ size_t scan_workspace(const selinv_scan_inputs *a, bool backward)
     return scan_space(*a, scan_spread(*a, backward), backward).total;
 }
 
-selinv_status scan_args(const selinv_scan_inputs &a, const Spread &s, bool backward, ScanArgs &p)
+selinv_status scan_args(const selinv_scan_inputs &a, const Spread &s, ScanArgs &p)
 {
     const size_t es = elem(a.dtype);
     const int64_t per = a.groups > 1 ? a.d / a.groups : 0;
-    const int cw = with_type(a.dtype, [&](auto t) { return scan_tile_channels<decltype(t)>((int)a.n, s.narrow, backward); });
-    if (a.lines * s.segs > MAX_GRID_X || a.groups * div_up(div_up(a.d / a.groups, cw), SCAN_BLOCK_TILES) > MAX_GRID_Y)
+    if (a.lines * s.segs > MAX_GRID_X ||
+        a.groups * div_up(div_up(a.d / a.groups, tile_channels(a, s.narrow)), SCAN_BLOCK_TILES) > MAX_GRID_Y)
         return SELINV_ERR_UNSUPPORTED;
     const size_t pack = es == 2 ? 8 : 16;        // B and C: four elements at a time, two in float64
     p.rows = Rows{a.table, a.live, a.rows};
@@ -260,7 +259,7 @@ selinv_status selinv_selective_scan(const selinv_scan_inputs *a, const selinv_vi
     const ScanSpace w = scan_space(*a, spread, false);
     if (w.total > 0 && (!workspace || workspace_bytes < w.total)) return SELINV_ERR_WORKSPACE;
     ScanArgs p{};
-    st = scan_args(*a, spread, false, p);
+    st = scan_args(*a, spread, p);
     if (st != SELINV_OK) return st;
     p.y = out_of(*y, es, a->groups > 1 ? a->d / a->groups : 0);
     p.state_out = state_out, p.kept = kept;
@@ -294,7 +293,7 @@ selinv_status selinv_selective_scan_backward(const selinv_scan_inputs *a, const 
     const ScanSpace w = scan_space(*a, spread, true);
     if (!workspace || workspace_bytes < w.total) return SELINV_ERR_WORKSPACE;
     ScanArgs p{};
-    st = scan_args(*a, spread, true, p);
+    st = scan_args(*a, spread, p);
     if (st != SELINV_OK) return st;
     char *ws = static_cast<char *>(workspace);
     p.ends = ws + w.ends, p.sums = ws + w.sums;
@@ -312,7 +311,7 @@ selinv_status selinv_selective_scan_backward(const selinv_scan_inputs *a, const 
     const int64_t sums = div_up(a->lines * a->rows * a->groups * 2 * scan_padded((int)a->n), 256) +
                          div_up(a->d * (a->n + 2), 32);
     if (sums > MAX_GRID_X) return SELINV_ERR_UNSUPPORTED;
-    return from_cuda(with_type(a->dtype, [&](auto t) { return scan_backward_launch<decltype(t)>(p, o, spread.narrow, s); }));
+    return from_cuda(with_type(a->dtype, [&](auto t) { return scan_backward_launch<decltype(t)>(p, o, s); }));
 }
 
 selinv_status selinv_selective_scan_step(const selinv_scan_step *a, void *stream)

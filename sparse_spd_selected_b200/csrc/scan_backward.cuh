@@ -6,11 +6,15 @@
 //   Bb = sum_d g dt' x              Cb = sum_d h yb'             Db = sum_t yb' x
 //   zb = yb silu'(z) (h . C + D x)  dtb = dt'b softplus'(dt + dt_bias).
 // A block works on SCAN_WARPS neighbouring warp tiles of channels and one
-// segment of a line, SCAN_R rows at a time from the end: the states inside
-// come again from the one kept before those rows, and wait in shared memory.
-// The sums over channels (Bb, Cb) leave a block as one partial sum per row,
-// those over rows (Ab, Db, dt_biasb) as one per segment; scan_sums_kernel
-// adds them in a fixed order.
+// segment of a line, SCAN_R rows at a time from the end.  The states inside
+// come again from the one kept before those rows: a first run leaves every
+// SCAN_S-th in shared memory, a second one fills the registers with the
+// states and decays of SCAN_S rows, which the backward recurrence then uses
+// up.  The sums over states and over channels go through shared memory, not
+// shuffles: one store of 16 bytes per thread and row, added by the lanes that
+// finish the rows.  The sums over channels (Bb, Cb) leave a block as one
+// partial sum per row, those over rows (Ab, Db, dt_biasb) as one per segment;
+// scan_sums_kernel adds them in a fixed order.
 #pragma once
 
 #include "scan.cuh"
@@ -18,12 +22,16 @@
 namespace selinv {
 namespace {
 
+constexpr int SCAN_S = 4;       // rows whose states and decays are in registers together
+
 template <class K> struct ScanBwdSmem {
     using C = typename K::C;
-    C dt[SCAN_R][K::PITCH], u[SCAN_R][K::PITCH], yb[SCAN_R][K::PITCH];
-    C gb[SCAN_R][K::PITCH], qa[SCAN_R][K::PITCH], hc[SCAN_R][K::PITCH];
-    C bc[SCAN_R][2 * K::NP];                                     // this warp's sums for Bb and Cb
-    typename K::V h[SCAN_R][K::TP * K::TN / 2][32][2];           // states after each row, by thread
+    using V = typename K::V;
+    C dt[SCAN_R][K::CW], u[SCAN_R][K::CW], yb[SCAN_R][K::CW];
+    C gb[SCAN_S][K::LN][K::CW], qa[SCAN_S][K::LN][K::CW], hc[SCAN_S][K::LN][K::CW];     // parts of the sums over states
+    C part[SCAN_S][K::LN][2 * K::TN / K::TD][K::LD][K::TD];     // parts of the sums over channels: B's states, then C's
+    C bc[SCAN_R][2 * K::NP];                                    // those sums of this warp
+    V h[SCAN_R / SCAN_S - 1][K::TP * K::TN][32];                // states before rows SCAN_S, 2 SCAN_S, ...
 };
 template <class K> struct ScanBwdBlock {
     using C = typename K::C;
@@ -31,388 +39,517 @@ template <class K> struct ScanBwdBlock {
     C b[SCAN_R][2 * K::NP], c[SCAN_R][2 * K::NP];
 };
 
-// MAIN: all outputs.  Otherwise only what each segment hands to the row before it: a g from nothing behind it, and the
-// sum of its steps.
-template <class K, bool MAIN>
+// a and h of row t.
+template <class K, bool POLY, int ROW>
+SELINV_DEVINL void scan_again(const ScanBwdSmem<K> &sm, const ScanBwdBlock<K> &block, int t, int d0, int n0, int n,
+                              const typename K::V (*A2)[K::TN], typename K::V (*h)[K::TN], typename K::V (*a)[K::TN])
+{
+    using V = typename K::V;
+    using C = typename K::C;
+    V dt2[K::TP], u2[K::TP], b2[K::TN];
+    get<K::TP>(&sm.dt[t][d0], dt2);
+    get<K::TP>(&sm.u[t][d0], u2);
+    get<K::TN>(&block.b[t][2 * n0], b2);
+    scan_pairs<K, POLY, ROW>([&](auto poly, int q, int j) {
+        a[q][j] = decay2<poly.value>(mul2(dt2[q], A2[q][j]));
+        h[q][j] = fma2(a[q][j], h[q][j], mul2(u2[q], b2[j]));
+    });
+    if (n < K::NP) {
+#pragma unroll
+        for (int j = 0; j < K::TN; ++j)
+            if (n0 + j >= n) {
+#pragma unroll
+                for (int q = 0; q < K::TP; ++q) h[q][j] = make2((C)0, (C)0);
+            }
+    }
+}
+
+// What a thread of the backward knows of its place.
+template <class K> struct ScanBwd {
+    using T = typename K::T;
+    using C = typename K::C;
+    using V = typename K::V;
+    const ScanArgs &p;
+    const ScanGrads &o;
+    ScanBwdBlock<K> &block;
+    ScanBwdSmem<K> &sm;
+    int lane, nl, d0, n0, nch;
+    int64_t line, part, dn;         // part: the warp's first channel in a [d, n] array
+
+    SELINV_DEVINL void states(const void *from, int64_t sequence, V (*v)[K::TN]) const
+    {
+        if (from)
+            load_part<K>(static_cast<const C *>(from) + p.rows.number(sequence, line) * dn + part, p.n, nch, lane, v);
+        else
+            zero_part<K>(v);
+    }
+    // The live sequence of row t of a tile whose first row lies in k0; st: the rows that begin one.
+    SELINV_DEVINL static int64_t sequence(int64_t k0, uint32_t st, int t) { return k0 + __popc(st & ((2u << t) - 2u)); }
+
+    // Rows t0 .. t0 + SCAN_S - 1, `before` the state before them.  EDGE: some row begins or ends a sequence; st has the
+    // rows that begin one and the row behind the last, of which only those below nr are rows.
+    template <bool POLY, bool EDGE>
+    SELINV_DEVINL void rows(int t0, int nr, uint32_t st, int64_t k0, const V (*A2)[K::TN], const V (*before)[K::TN], V (*g)[K::TN],
+                            V (*ab)[K::TN]) const
+    {
+        constexpr int S = SCAN_S, TP = K::TP, TN = K::TN;
+        V h[S][TP][TN], a[S][TP][TN];
+        const uint32_t begins = st & ((1u << nr) - 1u);
+        run<POLY, EDGE, 0>(t0, begins, k0, A2, before, h, a);
+#pragma unroll
+        for (int r = S - 1; r >= 0; --r) {
+            const int t = t0 + r;
+            if (EDGE && ((st >> (t + 1)) & 1u)) states(o.stateb, sequence(k0, st, t), g);
+            const bool first = EDGE && ((begins >> t) & 1u);
+            V start[TP][TN];
+            if (EDGE) {
+                if (first) {
+                    states(p.state, sequence(k0, st, t), start);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < TP; ++q)
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) start[q][j] = r > 0 ? h[r > 0 ? r - 1 : 0][q][j] : before[q][j];
+                }
+            }
+            V dt2[TP], u2[TP], yb2[TP], b2[TN], c2[TN], gb[TP], qa[TP];
+            get<TP>(&sm.dt[t][d0], dt2);
+            get<TP>(&sm.u[t][d0], u2);
+            get<TP>(&sm.yb[t][d0], yb2);
+            get<TN>(&block.b[t][2 * n0], b2);
+            get<TN>(&block.c[t][2 * n0], c2);
+            C sum[2 * TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                V sb, sc;
+#pragma unroll
+                for (int q = 0; q < TP; ++q) {
+                    const V past = EDGE ? start[q][j] : r > 0 ? h[r > 0 ? r - 1 : 0][q][j] : before[q][j];
+                    const V gt = fma2(c2[j], yb2[q], g[q][j]);
+                    sb = q ? fma2(gt, u2[q], sb) : mul2(gt, u2[q]);
+                    sc = q ? fma2(h[r][q][j], yb2[q], sc) : mul2(h[r][q][j], yb2[q]);
+                    gb[q] = j ? fma2(gt, b2[j], gb[q]) : mul2(gt, b2[j]);
+                    g[q][j] = mul2(a[r][q][j], gt);
+                    const V m = mul2(g[q][j], past);
+                    qa[q] = j ? fma2(m, A2[q][j], qa[q]) : mul2(m, A2[q][j]);
+                    ab[q][j] = fma2(m, dt2[q], ab[q][j]);
+                }
+                sum[j] = sb.x + sb.y, sum[TN + j] = sc.x + sc.y;
+            }
+            if (p.n < K::NP) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    if (n0 + j >= p.n) {
+#pragma unroll
+                        for (int q = 0; q < TP; ++q) g[q][j] = make2((C)0, (C)0);
+                    }
+            }
+            put<TP>(&sm.gb[r][nl][d0], gb);
+            put<TP>(&sm.qa[r][nl][d0], qa);
+            if (p.z.p) {
+                V hc[TP];
+#pragma unroll
+                for (int q = 0; q < TP; ++q) {
+                    hc[q] = mul2(c2[0], h[r][q][0]);
+#pragma unroll
+                    for (int j = 1; j < TN; ++j) hc[q] = fma2(c2[j], h[r][q][j], hc[q]);
+                }
+                put<TP>(&sm.hc[r][nl][d0], hc);
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * TN / K::TD; ++i) put<K::TD>(&sm.part[r][nl][i][lane % K::LD][0], sum + i * K::TD);
+            if (first && o.stateb_out)
+                store_part<K>(static_cast<C *>(o.stateb_out) + p.rows.number(sequence(k0, st, t), line) * dn + part, p.n, nch,
+                              lane, g);
+        }
+    }
+    // The states and decays of rows t0 + R on.
+    template <bool POLY, bool EDGE, int R>
+    SELINV_DEVINL void run(int t0, uint32_t st, int64_t k0, const V (*A2)[K::TN], const V (*before)[K::TN],
+                           V (*h)[K::TP][K::TN], V (*a)[K::TP][K::TN]) const
+    {
+        if constexpr (R < SCAN_S) {
+#pragma unroll
+            for (int q = 0; q < K::TP; ++q)
+#pragma unroll
+                for (int j = 0; j < K::TN; ++j) h[R][q][j] = R ? h[R ? R - 1 : 0][q][j] : before[q][j];
+            if (EDGE && ((st >> (t0 + R)) & 1u)) states(p.state, sequence(k0, st, t0 + R), h[R]);
+            scan_again<K, POLY, R>(sm, block, t0 + R, d0, n0, p.n, A2, h[R], a[R]);
+            run<POLY, EDGE, R + 1>(t0, st, k0, A2, before, h, a);
+        }
+    }
+    // SCAN_S rows of the first run.
+    template <bool POLY, bool EDGE, int R = 0>
+    SELINV_DEVINL void skip(int t0, uint32_t st, int64_t k0, const V (*A2)[K::TN], V (*h)[K::TN]) const
+    {
+        if constexpr (R < SCAN_S) {
+            V a[K::TP][K::TN];
+            if (EDGE && ((st >> (t0 + R)) & 1u)) states(p.state, sequence(k0, st, t0 + R), h);
+            scan_again<K, POLY, R>(sm, block, t0 + R, d0, n0, p.n, A2, h, a);
+            skip<POLY, EDGE, R + 1>(t0, st, k0, A2, h);
+        }
+    }
+};
+
+template <class K>
 __global__ void __launch_bounds__(SCAN_WARPS * 32)
     scan_backward_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ ScanGrads o)
 {
     using T = typename K::T;
     using C = typename K::C;
     using V = typename K::V;
-    constexpr int R = SCAN_R, CW = K::CW, E = K::E, EB = K::EB, NP = K::NP, TD = K::TD, TN = K::TN, TP = K::TP;
+    constexpr int R = SCAN_R, S = SCAN_S, LN = K::LN, LD = K::LD, NP = K::NP, TD = K::TD, TN = K::TN, TP = K::TP;
+    constexpr int PERS = S > LN ? S / LN : 1;       // rows of S that a lane finishes
     extern __shared__ __align__(16) char smem_raw[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     ScanBwdBlock<K> &block = *reinterpret_cast<ScanBwdBlock<K> *>(smem_raw);
-    ScanBwdSmem<K> *all = block.warp;
-    ScanBwdSmem<K> &sm = all[warp];
+    ScanBwdSmem<K> &sm = block.warp[warp];
     ScanPlace w;
     scan_place<K>(p, warp, w);              // a warp without channels (nch <= 0) still meets the others
-    const int nch = max(w.nch, 0);
-    if (nch == 0) w.c0 = 0;                 // its addresses are never used
+    w.nch = max(w.nch, 0);
+    if (w.nch == 0) w.c0 = 0;               // its addresses are never used
 
-    const int n = p.n, d0 = (lane / K::LN) * TD, n0 = (lane % K::LN) * TN;
-    const T *x = static_cast<const T *>(p.x.p) + w.line * p.x.line + w.c0;
-    const T *dt = static_cast<const T *>(p.dt.p) + w.line * p.dt.line + w.c0;
-    const T *z = p.z.p ? static_cast<const T *>(p.z.p) + w.line * p.z.line + w.c0 : nullptr;
+    const int n = p.n, nl = lane / LD, d0 = (lane % LD) * TD, n0 = nl * TN, nd = w.nch - d0;
+    const T *x = static_cast<const T *>(p.x.p) + w.line * p.x.line + w.c0 + d0;
+    const T *dt = static_cast<const T *>(p.dt.p) + w.line * p.dt.line + w.c0 + d0;
+    const T *z = p.z.p ? static_cast<const T *>(p.z.p) + w.line * p.z.line + w.c0 + d0 : nullptr;
     const T *B = static_cast<const T *>(p.B.p) + w.line * p.B.line + w.group * p.B_group;
     const T *Cc = static_cast<const T *>(p.C.p) + w.line * p.C.line + w.group * p.C_group;
-    const T *yb = static_cast<const T *>(o.yb.p) + w.line * o.yb.line + w.c0;
-    T *xb = static_cast<T *>(o.xb.p) + w.line * o.xb.line + w.c0;
-    T *dtb = static_cast<T *>(o.dtb.p) + w.line * o.dtb.line + w.c0;
-    T *zb = o.zb.p ? static_cast<T *>(o.zb.p) + w.line * o.zb.line + w.c0 : nullptr;
+    const T *yb = static_cast<const T *>(o.yb.p) + w.line * o.yb.line + w.c0 + d0;
+    T *xb = static_cast<T *>(o.xb.p) + w.line * o.xb.line + w.c0 + d0;
+    T *dtb = static_cast<T *>(o.dtb.p) + w.line * o.dtb.line + w.c0 + d0;
+    T *zb = o.zb.p ? static_cast<T *>(o.zb.p) + w.line * o.zb.line + w.c0 + d0 : nullptr;
     const int64_t part = (int64_t)w.c0 * n, dn = p.d * n;
-    const C *state = static_cast<const C *>(p.state), *stateb = static_cast<const C *>(o.stateb);
-    C *stateb_out = static_cast<C *>(o.stateb_out);
+    const ScanBwd<K> at{p, o, block, sm, lane, nl, d0, n0, w.nch, w.line, part, dn};
 
-    if (MAIN && stateb_out && p.rows.table && blockIdx.x == 0) {
+    if (o.stateb_out && p.rows.table && blockIdx.x == 0) {      // sequences without rows
+        C *out = static_cast<C *>(o.stateb_out);
+        const C *in = static_cast<const C *>(o.stateb);
         for (int64_t e = 0; e < p.sequences - p.rows.live; ++e) {
-            const int64_t at = p.rows.table[2 * p.rows.live + 1 + e] * dn + part;
-            for (int i = lane; i < nch * n; i += 32) stateb_out[at + i] = stateb ? stateb[at + i] : (C)0;
+            const int64_t a = p.rows.table[2 * p.rows.live + 1 + e] * dn + part;
+            for (int i = lane; i < w.nch * n; i += 32) out[a + i] = in ? in[a + i] : (C)0;
         }
     }
 
     V A2[TP][TN], g[TP][TN], ab[TP][TN];       // g: what the row behind hands on, a_{t+1} g_{t+1}
-    load_part<K>(static_cast<const C *>(p.A) + part, n, nch, lane, A2, (C)0);
+    V bias[TP], skip[TP], sum_d[TP], sum_bias[TP];
+    const bool plain = load_decay<K>(p.A, part, n, w.nch, lane, A2) && p.softplus;
+    zero_part<K>(g);
+    zero_part<K>(ab);
 #pragma unroll
-    for (int q = 0; q < TP; ++q)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            A2[q][j] = mul2(A2[q][j], make2(log2e<C>(), log2e<C>()));
-            g[q][j] = ab[q][j] = make2((C)0, (C)0);
-        }
-    const int ce = (lane % (CW / E)) * E;
-    C bias[E], skip[E], sum_d[E], sum_bias[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const bool in = ce + e < nch;
-        bias[e] = in && p.dt_bias ? static_cast<const C *>(p.dt_bias)[w.c0 + ce + e] : (C)0;
-        skip[e] = in && p.D ? static_cast<const C *>(p.D)[w.c0 + ce + e] : (C)0;
-        sum_d[e] = sum_bias[e] = 0;
+    for (int q = 0; q < TP; ++q) {
+        bias[q] = pair_of<K>(p.dt_bias, w.c0 + d0, nd, q);
+        skip[q] = pair_of<K>(p.D, w.c0 + d0, nd, q);
+        sum_d[q] = sum_bias[q] = make2((C)0, (C)0);
     }
-    V total[TP];
-#pragma unroll
-    for (int q = 0; q < TP; ++q) total[q] = make2((C)0, (C)0);
-
-    int64_t k = w.r1 > w.r0 ? p.rows.find(w.r1 - 1) : 0;     // the sequence of the row at hand
-    if (MAIN && w.r1 > w.r0 && p.rows.end(k) > w.r1) {
-        // what the segments behind this one hand on, from the last that holds rows of this sequence
-        const C *ends = static_cast<const C *>(p.ends) + w.line * p.segs * dn + part;
-        const C *sums = static_cast<const C *>(p.sums) + w.line * p.segs * p.d + w.c0;
-        int s = (int)((p.rows.end(k) - 1) / p.seg_rows);
-        load_part<K>(ends + s * dn, n, nch, lane, g, (C)0);
-        for (--s; s > w.seg; --s) {
-            V e[TP][TN];
-            load_part<K>(ends + s * dn, n, nch, lane, e, (C)0);
-#pragma unroll
-            for (int q = 0; q < TP; ++q) {
-                V t;
-                t.x = d0 + 2 * q < nch ? sums[s * p.d + d0 + 2 * q] : (C)0;
-                t.y = d0 + 2 * q + 1 < nch ? sums[s * p.d + d0 + 2 * q + 1] : (C)0;
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const V a = mul2(t, A2[q][j]);
-                    g[q][j] = fma2(make2(exp2_(a.x), exp2_(a.y)), g[q][j], e[q][j]);
-                }
-            }
-        }
-    }
-    const bool pad_n = n < NP;
+    int64_t k0 = w.r1 > w.r0 ? p.rows.find(w.r1 - 1) : 0;
+    if (w.r1 > w.r0 && p.rows.end(k0) > w.r1)       // what the segments behind this one hand on
+        scan_join<K>(p, w, (int)((p.rows.end(k0) - 1) / p.seg_rows), w.seg, -1, lane, A2, g);
     const int64_t tiles = (p.rows.rows + R - 1) / R;
+    const int per = (int)(p.d / p.groups), tiles_c = (per + K::CW - 1) / K::CW;
+    const int blocks = (tiles_c + SCAN_WARPS - 1) / SCAN_WARPS, bi = (int)blockIdx.y % blocks;
+    const int live = min(SCAN_WARPS, tiles_c - bi * SCAN_WARPS);
+    C *part_bc = static_cast<C *>(o.part_bc) +
+                 (((int64_t)bi * p.lines + w.line) * p.rows.rows * p.groups + w.group) * 2 * NP;
 
     for (int64_t rt = w.r0 + (w.r1 > w.r0 ? (w.r1 - w.r0 - 1) / R * R : 0); rt >= w.r0 && rt < w.r1; rt -= R) {
         const int nr = (int)min((int64_t)R, w.r1 - rt);
-        // the live sequence of this tile's first row, and the rows that begin one
-        int64_t k0 = k;
-        while (p.rows.start(k0) > rt) --k0;
+        while (p.rows.start(k0) > rt) --k0;         // the live sequence of this tile's first row
         const uint32_t st = p.rows.starts(rt, R, k0, lane);
-        // stage
+        // stage; rows that are not there (behind the last) change nothing: no step, no input, no cotangent
+        {
+            ScanLoad<K> xl, dl, yl, zl;
+            ScanLoadN<K, SCAN_WARPS * 32> bl, cl;
+            dl.load(dt, p.dt.row, rt, w.r1, nd, p.dt.wide, nl);
+            xl.load(x, p.x.row, rt, w.r1, nd, p.x.wide, nl);
+            yl.load(yb, o.yb.row, rt, w.r1, nd, o.yb.wide, nl);
+            if (z) zl.load(z, p.z.row, rt, w.r1, nd, p.z.wide, nl);
+            bl.load(B, p.B.row, rt, w.r1, n, p.B.wide, threadIdx.x);
+            cl.load(Cc, p.C.row, rt, w.r1, n, p.C.wide, threadIdx.x);
 #pragma unroll
-        for (int i = 0; i < K::PER; ++i) {
-            const int row = (lane + 32 * i) / (CW / E);
-            if (row >= R) break;
-            C a[E], b[E], c[E];
-            Pack<T, E> xv, dv, yv, zv;
-            xv.clear(), dv.clear(), yv.clear(), zv.clear();
-            if (row < nr && nch > 0) {
-                xv.load(x + (rt + row) * p.x.row + ce, nch - ce, p.x.wide);
-                dv.load(dt + (rt + row) * p.dt.row + ce, nch - ce, p.dt.wide);
-                yv.load(yb + (rt + row) * o.yb.row + ce, nch - ce, o.yb.wide);
-                if (z) zv.load(z + (rt + row) * p.z.row + ce, nch - ce, p.z.wide);
-            }
+            for (int i = 0; i < K::PER; ++i) {
+                const int row = nl + LN * i;
+                if (row >= R) break;
+                V a[TP], b[TP], c[TP];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                a[e] = dv.get(e) + bias[e];
-                if (p.softplus) a[e] = softplus_(a[e]);
-                b[e] = a[e] * xv.get(e);
-                c[e] = yv.get(e);
-                if (z) c[e] *= zv.get(e) * sigmoid_(zv.get(e));
-            }
-            put<E>(&sm.dt[row][ce], a);
-            put<E>(&sm.u[row][ce], b);
-            put<E>(&sm.yb[row][ce], c);
-        }
-#pragma unroll
-        for (int i = 0; i < (K::BVECS + SCAN_WARPS * 32 - 1) / (SCAN_WARPS * 32); ++i) {
-            const int vec = threadIdx.x + SCAN_WARPS * 32 * i, row = vec / (NP / EB), e0 = (vec % (NP / EB)) * EB;
-            if (row >= R) break;
-            C a[2 * EB], b[2 * EB];
-            Pack<T, EB> bv, cv;
-            bv.clear(), cv.clear();
-            if (row < nr) {
-                if (MAIN) bv.load(B + (rt + row) * p.B.row + e0, n - e0, p.B.wide);
-                cv.load(Cc + (rt + row) * p.C.row + e0, n - e0, p.C.wide);
-            }
-#pragma unroll
-            for (int e = 0; e < EB; ++e) {
-                a[2 * e] = a[2 * e + 1] = bv.get(e);
-                b[2 * e] = b[2 * e + 1] = cv.get(e);
-            }
-            if (MAIN) put<2 * EB>(&block.b[row][2 * e0], a);
-            put<2 * EB>(&block.c[row][2 * e0], b);
-        }
-        __syncthreads();
-        V h[TP][TN];
-        if (MAIN) {
-            // the states after each row but the last, again
-            load_part<K>(static_cast<const C *>(o.kept) + (w.line * tiles + rt / R) * dn + part, n, nch, lane, h, (C)0);
-            int64_t kk = k0;
-            for (int t = 0; t < nr; ++t) {
-                if ((st >> t) & 1u) {
-                    if (rt + t > p.rows.start(kk)) ++kk;
-                    if (state) {
-                        load_part<K>(state + p.rows.number(kk, w.line) * dn + part, n, nch, lane, h, (C)0);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < TP; ++q)
-#pragma unroll
-                            for (int j = 0; j < TN; ++j) h[q][j] = make2((C)0, (C)0);
+                for (int q = 0; q < TP; ++q) {
+                    a[q] = add2(make2(dl.v[i].get(2 * q), dl.v[i].get(2 * q + 1)), bias[q]);
+                    if (p.softplus) a[q] = softplus2(a[q]);
+                    if (row >= nr) a[q] = make2((C)0, (C)0);
+                    b[q] = mul2(a[q], make2(xl.v[i].get(2 * q), xl.v[i].get(2 * q + 1)));
+                    c[q] = make2(yl.v[i].get(2 * q), yl.v[i].get(2 * q + 1));
+                    if (z) {
+                        const V v = make2(zl.v[i].get(2 * q), zl.v[i].get(2 * q + 1));
+                        c[q] = mul2(c[q], mul2(v, sigmoid2(v)));
                     }
                 }
-                V dt2[TP], u2[TP], b2[TN];
-                get<TP>(&sm.dt[t][d0], dt2);
-                get<TP>(&sm.u[t][d0], u2);
-                get<TN>(&block.b[t][2 * n0], b2);
+                put<TP>(&sm.dt[row][d0], a);
+                put<TP>(&sm.u[row][d0], b);
+                put<TP>(&sm.yb[row][d0], c);
+            }
+            bl.stage(block.b, threadIdx.x);
+            cl.stage(block.c, threadIdx.x);
+        }
+        __syncthreads();
+
+        V h[TP][TN];
+        const C *kept = static_cast<const C *>(o.kept) + (w.line * tiles + rt / R) * dn + part;
+        load_part<K>(kept, n, w.nch, lane, h);
+        for (int b = 0; b < R / S - 1 && (b + 1) * S < nr; ++b) {
+            if ((st >> (b * S)) & ((1u << S) - 1u))
+                at.template skip<false, true>(b * S, st, k0, A2, h);
+            else if (plain)
+                at.template skip<true, false>(b * S, st, k0, A2, h);
+            else
+                at.template skip<false, false>(b * S, st, k0, A2, h);
+#pragma unroll
+            for (int q = 0; q < TP; ++q)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) sm.h[b][q * TN + j][lane] = h[q][j];
+        }
+        for (int b = (nr - 1) / S; b >= 0; --b) {
+            const int t0 = b * S;
+            if (b > 0) {
 #pragma unroll
                 for (int q = 0; q < TP; ++q)
 #pragma unroll
-                    for (int j = 0; j < TN; ++j) {
-                        const V e = mul2(dt2[q], A2[q][j]);
-                        h[q][j] = fma2(make2(exp2_(e.x), exp2_(e.y)), h[q][j], mul2(u2[q], b2[j]));
-                        if (pad_n && n0 + j >= n) h[q][j] = make2((C)0, (C)0);
-                    }
-#pragma unroll
-                for (int i = 0; i < TP * TN; ++i) sm.h[t][i / 2][lane][i % 2] = h[i / TN][i % TN];
-            }
-        }
-        // from the last row to the first
-        for (int t = nr - 1; t >= 0; --t) {
-            if ((st >> (t + 1)) & 1u) {         // the last row of its sequence
-                if (rt + t < p.rows.start(k)) --k;
-                if (stateb) {
-                    load_part<K>(stateb + p.rows.number(k, w.line) * dn + part, n, nch, lane, g, (C)0);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < TP; ++q)
-#pragma unroll
-                        for (int j = 0; j < TN; ++j) g[q][j] = make2((C)0, (C)0);
-                }
-            }
-            const bool first = (st >> t) & 1u;
-            V dt2[TP], yb2[TP], c2[TN];
-            get<TP>(&sm.dt[t][d0], dt2);
-            get<TP>(&sm.yb[t][d0], yb2);
-            get<TN>(&block.c[t][2 * n0], c2);
-            if constexpr (!MAIN) {
-#pragma unroll
-                for (int q = 0; q < TP; ++q) {
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) {
-                        const V e = mul2(dt2[q], A2[q][j]);
-                        g[q][j] = mul2(make2(exp2_(e.x), exp2_(e.y)), fma2(c2[j], yb2[q], g[q][j]));
-                    }
-                    total[q] = add2(total[q], dt2[q]);
-                }
+                    for (int j = 0; j < TN; ++j) h[q][j] = sm.h[b - 1][q * TN + j][lane];
             } else {
-                V u2[TP], b2[TN], past[TP][TN], gb[TP], qa[TP], hc[TP];
-                C bc[2 * TN];
-                get<TP>(&sm.u[t][d0], u2);
-                get<TN>(&block.b[t][2 * n0], b2);
-                if (first) {
-                    if (state) {
-                        load_part<K>(state + p.rows.number(k, w.line) * dn + part, n, nch, lane, past, (C)0);
-                    } else {
+                load_part<K>(kept, n, w.nch, lane, h);
+            }
+            Pack<T, TD> xv[PERS], dv[PERS], yv[PERS], zv[PERS];
 #pragma unroll
-                        for (int q = 0; q < TP; ++q)
-#pragma unroll
-                            for (int j = 0; j < TN; ++j) past[q][j] = make2((C)0, (C)0);
-                    }
-                } else if (t > 0) {
-#pragma unroll
-                    for (int i = 0; i < TP * TN; ++i) past[i / TN][i % TN] = sm.h[t - 1][i / 2][lane][i % 2];
-                } else {
-                    load_part<K>(static_cast<const C *>(o.kept) + (w.line * tiles + rt / R) * dn + part, n, nch, lane,
-                                 past, (C)0);
-                }
-#pragma unroll
-                for (int q = 0; q < TP; ++q) gb[q] = qa[q] = hc[q] = make2((C)0, (C)0);
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    V sb = make2((C)0, (C)0), sc = make2((C)0, (C)0);
-#pragma unroll
-                    for (int q = 0; q < TP; ++q) {
-                        const V e = mul2(dt2[q], A2[q][j]);
-                        const V a = make2(exp2_(e.x), exp2_(e.y));
-                        const V gt = fma2(c2[j], yb2[q], g[q][j]);
-                        sb = fma2(gt, u2[q], sb);
-                        sc = fma2(h[q][j], yb2[q], sc);
-                        gb[q] = fma2(gt, b2[j], gb[q]);
-                        hc[q] = fma2(h[q][j], c2[j], hc[q]);
-                        g[q][j] = mul2(a, gt);
-                        const V m = mul2(g[q][j], past[q][j]);
-                        qa[q] = fma2(m, A2[q][j], qa[q]);
-                        ab[q][j] = fma2(m, dt2[q], ab[q][j]);
-                        h[q][j] = past[q][j];
-                        if (pad_n && n0 + j >= n) g[q][j] = make2((C)0, (C)0);
-                    }
-                    bc[j] = sb.x + sb.y, bc[TN + j] = sc.x + sc.y;
-                }
-                if (first) {
-                    if (stateb_out) store_part<K>(stateb_out + p.rows.number(k, w.line) * dn + part, n, nch, lane, g);
-                    // the row before is another sequence's last
-                    if (t > 0) {
-#pragma unroll
-                        for (int i = 0; i < TP * TN; ++i) h[i / TN][i % TN] = sm.h[t - 1][i / 2][lane][i % 2];
-                    }
-                }
-                scatter_sum<2 * TN, K::LN, 32>(bc, lane);
-                {
-                    constexpr int KEEP = 2 * TN > K::LD ? 2 * TN / K::LD : 1;
-                    if (scatter_writes<2 * TN, K::LN, 32>(lane)) {
-                        const int f = scatter_first<2 * TN, K::LN, 32>(lane);
-#pragma unroll
-                        for (int i = 0; i < KEEP; ++i) sm.bc[t][((f + i) / TN) * NP + n0 + (f + i) % TN] = bc[i];
-                    }
-                }
-                C v[TD * 2], y1[TD];
-#pragma unroll
-                for (int q = 0; q < TP; ++q) {
-                    v[2 * q] = gb[q].x, v[2 * q + 1] = gb[q].y;
-                    v[TD + 2 * q] = qa[q].x, v[TD + 2 * q + 1] = qa[q].y;
-                    y1[2 * q] = hc[q].x, y1[2 * q + 1] = hc[q].y;
-                }
-                scatter_sum<2 * TD, 1, K::LN>(v, lane);
-                {
-                    constexpr int KEEP = 2 * TD > K::LN ? 2 * TD / K::LN : 1;
-                    if (scatter_writes<2 * TD, 1, K::LN>(lane)) {
-                        const int f = scatter_first<2 * TD, 1, K::LN>(lane);
-#pragma unroll
-                        for (int i = 0; i < KEEP; ++i) {
-                            if (f + i < TD)
-                                sm.gb[t][d0 + f + i] = v[i];
-                            else
-                                sm.qa[t][d0 + f + i - TD] = v[i] * ln2<C>();
-                        }
-                    }
-                }
-                if (z) {
-                    scatter_sum<TD, 1, K::LN>(y1, lane);
-                    constexpr int KEEP = TD > K::LN ? TD / K::LN : 1;
-                    if (scatter_writes<TD, 1, K::LN>(lane)) {
-                        const int f = scatter_first<TD, 1, K::LN>(lane);
-#pragma unroll
-                        for (int i = 0; i < KEEP; ++i) sm.hc[t][d0 + f + i] = y1[i];
+            for (int i = 0; i < PERS; ++i) {
+                const int row = t0 + nl + LN * i;
+                xv[i].clear(), dv[i].clear(), yv[i].clear(), zv[i].clear();
+                if (nl < S && row < nr) {
+                    xv[i].load(x + (rt + row) * p.x.row, nd, p.x.wide);
+                    dv[i].load(dt + (rt + row) * p.dt.row, nd, p.dt.wide);
+                    if (z) {
+                        yv[i].load(yb + (rt + row) * o.yb.row, nd, o.yb.wide);
+                        zv[i].load(z + (rt + row) * p.z.row, nd, p.z.wide);
                     }
                 }
             }
-        }
-        k = k0;
-        __syncthreads();
-        if constexpr (MAIN) {
+            if ((st >> t0) & ((2u << S) - 1u))
+                at.template rows<false, true>(t0, nr, st, k0, A2, h, g, ab);
+            else if (plain)
+                at.template rows<true, false>(t0, nr, st, k0, A2, h, g, ab);
+            else
+                at.template rows<false, false>(t0, nr, st, k0, A2, h, g, ab);
+            __syncwarp();
+            // finish the rows: the sums over states
 #pragma unroll
-            for (int i = 0; i < K::PER; ++i) {
-                const int row = (lane + 32 * i) / (CW / E);
-                if (row >= nr || nch == 0) break;
-                Pack<T, E> xv, dv, yv, zv, out;
-                xv.load(x + (rt + row) * p.x.row + ce, nch - ce, p.x.wide);
-                dv.load(dt + (rt + row) * p.dt.row + ce, nch - ce, p.dt.wide);
-                C s[E], gb[E], qa[E], hc[E], xo[E], so[E], zo[E], ys[E];
-                get<E>(&sm.dt[row][ce], s);
-                get<E>(&sm.yb[row][ce], ys);
-                get<E>(&sm.gb[row][ce], gb);
-                get<E>(&sm.qa[row][ce], qa);
-                if (z) {
-                    get<E>(&sm.hc[row][ce], hc);
-                    yv.load(yb + (rt + row) * o.yb.row + ce, nch - ce, o.yb.wide);
-                    zv.load(z + (rt + row) * p.z.row + ce, nch - ce, p.z.wide);
-                }
+            for (int i = 0; i < PERS; ++i) {
+                const int r = nl + LN * i, row = t0 + r;
+                if (nl >= S || row >= nr) break;
+                V gb[TP], qa[TP], hc[TP], s[TP], ys[TP];
+                get<TP>(&sm.gb[r][nl][d0], gb);
+                get<TP>(&sm.qa[r][nl][d0], qa);
+                get<TP>(&sm.hc[r][nl][d0], hc);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const C xe = xv.get(e);
-                    xo[e] = gb[e] * s[e] + skip[e] * ys[e];
-                    so[e] = gb[e] * xe + qa[e];
-                    if (p.softplus) so[e] *= sigmoid_(dv.get(e) + bias[e]);
-                    sum_d[e] += ys[e] * xe;
-                    sum_bias[e] += so[e];
+                for (int e = 1; e < LN; ++e) {
+                    V v[TP];
+                    const int from = (nl + e) % LN;
+                    get<TP>(&sm.gb[r][from][d0], v);
+#pragma unroll
+                    for (int q = 0; q < TP; ++q) gb[q] = add2(gb[q], v[q]);
+                    get<TP>(&sm.qa[r][from][d0], v);
+#pragma unroll
+                    for (int q = 0; q < TP; ++q) qa[q] = add2(qa[q], v[q]);
                     if (z) {
-                        const C ze = zv.get(e);
-                        zo[e] = yv.get(e) * (hc[e] + skip[e] * xe) * silu_slope(ze, sigmoid_(ze));
+                        get<TP>(&sm.hc[r][from][d0], v);
+#pragma unroll
+                        for (int q = 0; q < TP; ++q) hc[q] = add2(hc[q], v[q]);
                     }
                 }
+                get<TP>(&sm.dt[row][d0], s);
+                get<TP>(&sm.yb[row][d0], ys);
+                C xo[TD], so[TD], zo[TD];
+#pragma unroll
+                for (int q = 0; q < TP; ++q) {
+                    const V xe = make2(xv[i].get(2 * q), xv[i].get(2 * q + 1));
+                    const V vx = fma2(gb[q], s[q], mul2(skip[q], ys[q]));
+                    V vs = fma2(qa[q], make2(ln2<C>(), ln2<C>()), mul2(gb[q], xe));
+                    if (p.softplus) vs = mul2(vs, sigmoid2(add2(make2(dv[i].get(2 * q), dv[i].get(2 * q + 1)), bias[q])));
+                    sum_d[q] = fma2(ys[q], xe, sum_d[q]);
+                    sum_bias[q] = add2(sum_bias[q], vs);
+                    xo[2 * q] = vx.x, xo[2 * q + 1] = vx.y;
+                    so[2 * q] = vs.x, so[2 * q + 1] = vs.y;
+                    if (z) {
+                        const V ze = make2(zv[i].get(2 * q), zv[i].get(2 * q + 1)), pe = sigmoid2(ze);
+                        const V vz = mul2(make2(yv[i].get(2 * q), yv[i].get(2 * q + 1)), fma2(skip[q], xe, hc[q]));
+                        zo[2 * q] = vz.x * silu_slope(ze.x, pe.x), zo[2 * q + 1] = vz.y * silu_slope(ze.y, pe.y);
+                    }
+                }
+                Pack<T, TD> out;
                 out.set(xo);
-                out.store(xb + (rt + row) * o.xb.row + ce, nch - ce, o.xb.wide);
+                out.store(xb + (rt + row) * o.xb.row, nd, o.xb.wide);
                 out.set(so);
-                out.store(dtb + (rt + row) * o.dtb.row + ce, nch - ce, o.dtb.wide);
+                out.store(dtb + (rt + row) * o.dtb.row, nd, o.dtb.wide);
                 if (z) {
                     out.set(zo);
-                    out.store(zb + (rt + row) * o.zb.row + ce, nch - ce, o.zb.wide);
+                    out.store(zb + (rt + row) * o.zb.row, nd, o.zb.wide);
                 }
             }
-            // Bb and Cb: the block's warps, in order, into this block's partial sums [blocks of a group][line, row][group]
-            const int per = (int)(p.d / p.groups), tiles_c = (per + CW - 1) / CW;
-            const int blocks = (tiles_c + SCAN_WARPS - 1) / SCAN_WARPS;
-            const int64_t all_rows = p.lines * p.rows.rows;
-            C *out = static_cast<C *>(o.part_bc) +
-                     (((int64_t)((int)blockIdx.y % blocks) * all_rows + w.line * p.rows.rows + rt) * p.groups + w.group) * 2 * NP;
-            const int live = min(SCAN_WARPS, tiles_c - ((int)blockIdx.y % blocks) * SCAN_WARPS);
-            for (int i = threadIdx.x; i < nr * 2 * NP; i += SCAN_WARPS * 32) {
-                const int t = i / (2 * NP), j = i % (2 * NP);
-                C v = all[0].bc[t][j];
-                for (int a = 1; a < live; ++a) v += all[a].bc[t][j];
-                out[(int64_t)t * p.groups * 2 * NP + j] = v;
+            // and the sums over this warp's channels: TD of a row's 2 NP values at a time, from another lane's part on
+            // each, so that the lanes read other banks
+            constexpr int QUADS = LN * (2 * TN / TD);
+            for (int i = lane; i < S * QUADS; i += 32) {
+                const int r = i / QUADS, quad = i % QUADS, m = quad / (2 * TN / TD), half = quad % (2 * TN / TD);
+                C v[TD], e[TD];
+                get<TD>(&sm.part[r][m][half][quad % LD][0], v);
+#pragma unroll
+                for (int f = 1; f < LD; ++f) {
+                    get<TD>(&sm.part[r][m][half][(quad + f) % LD][0], e);
+#pragma unroll
+                    for (int c = 0; c < TD; ++c) v[c] += e[c];
+                }
+#pragma unroll
+                for (int c = 0; c < TD; ++c) {
+                    const int j = half * TD + c;
+                    sm.bc[t0 + r][(j / TN) * NP + m * TN + j % TN] = v[c];
+                }
             }
-            __syncthreads();
+            __syncwarp();
+        }
+        __syncthreads();
+        // Bb and Cb: the block's warps, in order, into this block's partial sums [blocks of a group][line, row][group]
+        for (int i = threadIdx.x; i < nr * 2 * NP; i += SCAN_WARPS * 32) {
+            const int t = i / (2 * NP), j = i % (2 * NP);
+            C v = block.warp[0].bc[t][j];
+            for (int a = 1; a < live; ++a) v += block.warp[a].bc[t][j];
+            part_bc[(rt + t) * p.groups * 2 * NP + j] = v;
         }
     }
-    if (nch == 0) return;
-    const int64_t at = w.line * p.segs + w.seg;
-    if constexpr (!MAIN) {
-        C *ends = static_cast<C *>(p.ends) + at * dn + part;
-        C *sums = static_cast<C *>(p.sums) + at * p.d + w.c0;
-        store_part<K>(ends, n, nch, lane, g);
-        if (lane % K::LN == 0) {
+    if (w.nch == 0) return;
+    const int64_t piece = w.line * p.segs + w.seg;
+    store_part<K>(static_cast<C *>(o.part_a) + piece * dn + part, n, w.nch, lane, ab);
+    // lanes that finished the same channels
+    C *pd = static_cast<C *>(o.part_d) + piece * p.d + w.c0 + d0, *pb = static_cast<C *>(o.part_bias) + piece * p.d + w.c0 + d0;
+#pragma unroll
+    for (int q = 0; q < TP; ++q) {
+#pragma unroll
+        for (int m = LD; m < 32; m *= 2) {
+            sum_d[q] = add2(sum_d[q], make2(shfl_xor_(sum_d[q].x, m), shfl_xor_(sum_d[q].y, m)));
+            sum_bias[q] = add2(sum_bias[q], make2(shfl_xor_(sum_bias[q].x, m), shfl_xor_(sum_bias[q].y, m)));
+        }
+        if (nl == 0) {
+            if (2 * q < nd) pd[2 * q] = sum_d[q].x, pb[2 * q] = sum_bias[q].x;
+            if (2 * q + 1 < nd) pd[2 * q + 1] = sum_d[q].y, pb[2 * q + 1] = sum_bias[q].y;
+        }
+    }
+}
+
+// What each segment hands to the row before it, from nothing behind it, and the sum of its steps.
+template <class K> struct ScanEndsSmem {
+    using C = typename K::C;
+    C dt[SCAN_R][K::CW], yb[SCAN_R][K::CW], c[SCAN_R][2 * K::NP];
+};
+template <class K, bool POLY, int ROW>
+SELINV_DEVINL void scan_ends_row(const ScanEndsSmem<K> &sm, int t, int d0, int n0, const typename K::V (*A2)[K::TN],
+                                 typename K::V (*g)[K::TN], typename K::V *total)
+{
+    using V = typename K::V;
+    V dt2[K::TP], yb2[K::TP], c2[K::TN];
+    get<K::TP>(&sm.dt[t][d0], dt2);
+    get<K::TP>(&sm.yb[t][d0], yb2);
+    get<K::TN>(&sm.c[t][2 * n0], c2);
+    scan_pairs<K, POLY, ROW>([&](auto poly, int q, int j) {
+        g[q][j] = mul2(decay2<poly.value>(mul2(dt2[q], A2[q][j])), fma2(c2[j], yb2[q], g[q][j]));
+    });
+#pragma unroll
+    for (int q = 0; q < K::TP; ++q) total[q] = add2(total[q], dt2[q]);
+}
+template <class K>
+__global__ void __launch_bounds__(SCAN_WARPS * 32)
+    scan_backward_ends_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ ScanGrads o)
+{
+    using T = typename K::T;
+    using C = typename K::C;
+    using V = typename K::V;
+    constexpr int R = SCAN_R, LN = K::LN, TP = K::TP, TN = K::TN;
+    extern __shared__ __align__(16) char smem_raw[];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    ScanEndsSmem<K> &sm = reinterpret_cast<ScanEndsSmem<K> *>(smem_raw)[warp];
+    ScanPlace w;
+    if (!scan_place<K>(p, warp, w) || w.r0 >= w.r1 || w.seg == 0) return;
+    const int n = p.n, nl = lane / K::LD, d0 = (lane % K::LD) * K::TD, n0 = nl * TN, nd = w.nch - d0;
+    const T *dt = static_cast<const T *>(p.dt.p) + w.line * p.dt.line + w.c0 + d0;
+    const T *z = p.z.p ? static_cast<const T *>(p.z.p) + w.line * p.z.line + w.c0 + d0 : nullptr;
+    const T *Cc = static_cast<const T *>(p.C.p) + w.line * p.C.line + w.group * p.C_group;
+    const T *yb = static_cast<const T *>(o.yb.p) + w.line * o.yb.line + w.c0 + d0;
+    const int64_t part = (int64_t)w.c0 * n, dn = p.d * n;
+    V A2[TP][TN], g[TP][TN], bias[TP], total[TP];
+    const bool plain = load_decay<K>(p.A, part, n, w.nch, lane, A2) && p.softplus;
+    zero_part<K>(g);
+#pragma unroll
+    for (int q = 0; q < TP; ++q) {
+        bias[q] = pair_of<K>(p.dt_bias, w.c0 + d0, nd, q);
+        total[q] = make2((C)0, (C)0);
+    }
+    ScanLoad<K> dl, yl, zl;
+    ScanLoadN<K, 32> cl;
+    auto fetch = [&](int64_t r) {
+        dl.load(dt, p.dt.row, r, w.r1, nd, p.dt.wide, nl);
+        yl.load(yb, o.yb.row, r, w.r1, nd, o.yb.wide, nl);
+        if (z) zl.load(z, p.z.row, r, w.r1, nd, p.z.wide, nl);
+        cl.load(Cc, p.C.row, r, w.r1, n, p.C.wide, lane);
+    };
+    int64_t k = p.rows.find(w.r1 - 1);          // the sequence of the row at hand
+    int64_t rt = w.r0 + (w.r1 - w.r0 - 1) / R * R;
+    fetch(rt);
+    for (; rt >= w.r0; rt -= R) {
+        const int nr = (int)min((int64_t)R, w.r1 - rt);
+        int64_t k0 = k;
+        while (p.rows.start(k0) > rt) --k0;
+        const uint32_t st = p.rows.starts(rt, R, k0, lane);
+#pragma unroll
+        for (int i = 0; i < K::PER; ++i) {
+            const int row = nl + LN * i;
+            if (row >= R) break;
+            V a[TP], c[TP];
 #pragma unroll
             for (int q = 0; q < TP; ++q) {
-                if (d0 + 2 * q < nch) sums[d0 + 2 * q] = total[q].x;
-                if (d0 + 2 * q + 1 < nch) sums[d0 + 2 * q + 1] = total[q].y;
+                a[q] = add2(make2(dl.v[i].get(2 * q), dl.v[i].get(2 * q + 1)), bias[q]);
+                if (p.softplus) a[q] = softplus2(a[q]);
+                c[q] = make2(yl.v[i].get(2 * q), yl.v[i].get(2 * q + 1));
+                if (z) {
+                    const V v = make2(zl.v[i].get(2 * q), zl.v[i].get(2 * q + 1));
+                    c[q] = mul2(c[q], mul2(v, sigmoid2(v)));
+                }
             }
+            put<TP>(&sm.dt[row][d0], a);
+            put<TP>(&sm.yb[row][d0], c);
         }
-    } else {
-        store_part<K>(static_cast<C *>(o.part_a) + at * dn + part, n, nch, lane, ab);
-        // lanes that converted the same channels
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-#pragma unroll
-            for (int m = CW / E; m < 32; m *= 2) {
-                sum_d[e] += shfl_xor_(sum_d[e], m);
-                sum_bias[e] += shfl_xor_(sum_bias[e], m);
+        cl.stage(sm.c, lane);
+        if (rt > w.r0) fetch(rt - R);
+        __syncwarp();
+        for (int t = nr - 1; t >= 0;) {
+            if ((st >> (t + 1)) & 1u) {         // the last row of its sequence
+                if (rt + t < p.rows.start(k)) --k;
+                if (o.stateb)
+                    load_part<K>(static_cast<const C *>(o.stateb) + p.rows.number(k, w.line) * dn + part, n, w.nch, lane, g);
+                else
+                    zero_part<K>(g);
             }
-            if (lane < CW / E && ce + e < nch) {
-                static_cast<C *>(o.part_d)[at * p.d + w.c0 + ce + e] = sum_d[e];
-                static_cast<C *>(o.part_bias)[at * p.d + w.c0 + ce + e] = sum_bias[e];
+            // down to the row behind the next such row
+            const uint32_t earlier = st & ((2u << t) - 2u);
+            const int te = earlier ? 31 - __clz(earlier) : 0;
+            if (plain) {
+                for (; t - 3 >= te; t -= 4) {
+                    scan_ends_row<K, true, 3>(sm, t, d0, n0, A2, g, total);
+                    scan_ends_row<K, true, 2>(sm, t - 1, d0, n0, A2, g, total);
+                    scan_ends_row<K, true, 1>(sm, t - 2, d0, n0, A2, g, total);
+                    scan_ends_row<K, true, 0>(sm, t - 3, d0, n0, A2, g, total);
+                }
             }
+#pragma unroll 1
+            for (; t >= te; --t) scan_ends_row<K, false, 0>(sm, t, d0, n0, A2, g, total);
         }
+        __syncwarp();
     }
+    scan_leave<K>(p, w, lane, g, total);
 }
 
 // Bb and Cb from the blocks' sums, and Ab, Db, dt_biasb from the segments': the first `bc_blocks` blocks take one
@@ -476,20 +613,23 @@ template <class K> cudaError_t scan_backward_run(const ScanArgs &p, const ScanGr
     const int parts = scan_parts<K>(p);
     const dim3 grid((unsigned)(p.lines * p.segs), (unsigned)(p.groups * parts));
     static_assert(sizeof(ScanBwdSmem<K>) % 16 == 0 && offsetof(ScanBwdSmem<K>, h) % 16 == 0 &&
+                      offsetof(ScanBwdSmem<K>, gb) % 16 == 0 && offsetof(ScanBwdSmem<K>, qa) % 16 == 0 &&
+                      offsetof(ScanBwdSmem<K>, hc) % 16 == 0 && offsetof(ScanBwdSmem<K>, part) % 16 == 0 &&
                       offsetof(ScanBwdBlock<K>, b) % 16 == 0 && offsetof(ScanBwdBlock<K>, c) % 16 == 0,
                   "staged rows lie on 16 bytes");
     constexpr int bytes = (int)sizeof(ScanBwdBlock<K>);
     static_assert(bytes <= 227 * 1024, "fits an SM");
     if (p.segs > 1) {
+        constexpr int ends = SCAN_WARPS * (int)sizeof(ScanEndsSmem<K>);
+        static_assert(sizeof(ScanEndsSmem<K>) % 16 == 0 && offsetof(ScanEndsSmem<K>, c) % 16 == 0, "rows on 16 bytes");
         cudaError_t e =
-            cudaFuncSetAttribute(scan_backward_kernel<K, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            cudaFuncSetAttribute(scan_backward_ends_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, ends);
         if (e != cudaSuccess) return e;
-        scan_backward_kernel<K, false><<<grid, SCAN_WARPS * 32, bytes, s>>>(p, o);
+        scan_backward_ends_kernel<K><<<grid, SCAN_WARPS * 32, ends, s>>>(p, o);
     }
-    cudaError_t e =
-        cudaFuncSetAttribute(scan_backward_kernel<K, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(scan_backward_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    scan_backward_kernel<K, true><<<grid, SCAN_WARPS * 32, bytes, s>>>(p, o);
+    scan_backward_kernel<K><<<grid, SCAN_WARPS * 32, bytes, s>>>(p, o);
     const int64_t bc = (p.lines * p.rows.rows * p.groups * 2 * K::NP + 255) / 256;
     const int64_t params = (p.d * (p.n + 2) + 31) / 32;
     scan_sums_kernel<typename K::T, K::NP><<<(unsigned)(bc + params), 256, 0, s>>>(p, o, bc, parts);

@@ -12,43 +12,44 @@ static_assert(SCAN_R == SCAN_KEEP_ROWS && SCAN_WARPS == SCAN_BLOCK_TILES, "the h
 
 namespace {
 
-template <class T, int NP> struct Tiles {
-    using Narrow = ScanTile<T, 2, 2, NP / 2>;
-    using Wide = std::conditional_t<sizeof(T) == 8, Narrow, ScanTile<T, 4, 4, NP / 4>>;
+// The tile for n states: 4 channels x 4, 2 or 1 states per thread (float64: 2 x 2).  The backward takes the first.
+template <class T, int NP, int NARROW> struct TileOf {
+    static constexpr int TN = NARROW == 0 ? 4 : NARROW == 1 || NP == 64 ? 2 : 1;
+    using K = std::conditional_t<sizeof(T) == 8, ScanTile<T, 2, 2, NP>, ScanTile<T, 16 / sizeof(typename Elem<T>::C), TN, NP>>;
 };
-
-// Calls f with the tile type for n states; the backward keeps a tile's states in shared memory, where not every wide
-// tile fits.
-template <class T, bool BACKWARD, class F> auto with_tile(int n, bool narrow, F f)
+template <class T, int NP, class F> auto with_width_of(int narrow, F f)
 {
-    auto pick = [&](auto t) {
-        using P = decltype(t);
-        if constexpr (!std::is_same<typename P::Wide, typename P::Narrow>::value &&
-                      (!BACKWARD || sizeof(ScanBwdBlock<typename P::Wide>) <= 227 * 1024))
-            if (!narrow) return f(typename P::Wide());
-        return f(typename P::Narrow());
-    };
-    if (n <= 4) return pick(Tiles<T, 4>());
-    if (n <= 8) return pick(Tiles<T, 8>());
-    if (n <= 16) return pick(Tiles<T, 16>());
-    if (n <= 32) return pick(Tiles<T, 32>());
-    return pick(Tiles<T, 64>());
+    if (narrow == 0) return f(typename TileOf<T, NP, 0>::K());
+    if (narrow == 1) return f(typename TileOf<T, NP, 1>::K());
+    return f(typename TileOf<T, NP, 2>::K());
+}
+// Calls f with the tile type.
+template <class T, class F> auto with_tile(int n, int narrow, F f)
+{
+    if (n <= 4) return with_width_of<T, 4>(narrow, f);
+    if (n <= 8) return with_width_of<T, 8>(narrow, f);
+    if (n <= 16) return with_width_of<T, 16>(narrow, f);
+    if (n <= 32) return with_width_of<T, 32>(narrow, f);
+    return with_width_of<T, 64>(narrow, f);
 }
 
 }  // namespace
 
-template <class T> int scan_tile_channels(int n, bool narrow, bool backward)
+template <class T> int scan_tile_channels(int n, int narrow)
 {
-    const auto cw = [](auto k) { return decltype(k)::CW; };
-    return backward ? with_tile<T, true>(n, narrow, cw) : with_tile<T, false>(n, narrow, cw);
+    return with_tile<T>(n, narrow, [](auto k) { return decltype(k)::CW; });
 }
-template <class T> cudaError_t scan_launch(const ScanArgs &p, bool narrow, cudaStream_t s)
+template <class T> cudaError_t scan_launch(const ScanArgs &p, int narrow, cudaStream_t s)
 {
-    return with_tile<T, false>(p.n, narrow, [&](auto k) { return scan_run<decltype(k)>(p, s); });
+    return with_tile<T>(p.n, narrow, [&](auto k) { return scan_run<decltype(k)>(p, s); });
 }
-template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, bool narrow, cudaStream_t s)
+template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, cudaStream_t s)
 {
-    return with_tile<T, true>(p.n, narrow, [&](auto k) { return scan_backward_run<decltype(k)>(p, o, s); });
+    if (p.n <= 4) return scan_backward_run<typename TileOf<T, 4, 0>::K>(p, o, s);
+    if (p.n <= 8) return scan_backward_run<typename TileOf<T, 8, 0>::K>(p, o, s);
+    if (p.n <= 16) return scan_backward_run<typename TileOf<T, 16, 0>::K>(p, o, s);
+    if (p.n <= 32) return scan_backward_run<typename TileOf<T, 32, 0>::K>(p, o, s);
+    return scan_backward_run<typename TileOf<T, 64, 0>::K>(p, o, s);
 }
 template <class T> cudaError_t scan_step_launch(const ScanStepArgs &p, cudaStream_t s)
 {
@@ -59,10 +60,10 @@ template <class T> cudaError_t scan_step_launch(const ScanStepArgs &p, cudaStrea
     return scan_step_run<T, 16>(p, s);
 }
 
-#define SELINV_SCAN_INSTANCES(T)                                                            \
-    template int scan_tile_channels<T>(int, bool, bool);                                       \
-    template cudaError_t scan_launch<T>(const ScanArgs &, bool, cudaStream_t);              \
-    template cudaError_t scan_backward_launch<T>(const ScanArgs &, const ScanGrads &, bool, cudaStream_t); \
+#define SELINV_SCAN_INSTANCES(T)                                                                   \
+    template int scan_tile_channels<T>(int, int);                                                  \
+    template cudaError_t scan_launch<T>(const ScanArgs &, int, cudaStream_t);                      \
+    template cudaError_t scan_backward_launch<T>(const ScanArgs &, const ScanGrads &, cudaStream_t); \
     template cudaError_t scan_step_launch<T>(const ScanStepArgs &, cudaStream_t);
 
 }  // namespace selinv

@@ -204,34 +204,74 @@ SELINV_DEVINL float exp2_(float x)
     return r;
 }
 SELINV_DEVINL double exp2_(double x) { return exp2(x); }
-SELINV_DEVINL float rcp_(float x) { return __fdividef(1.0f, x); }
+SELINV_DEVINL float rcp_(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 SELINV_DEVINL double rcp_(double x) { return 1.0 / x; }
 
+// 2^e for a pair whose entries are at most zero, or NaN.  POLY: in the FMA pipe, for a part of the pairs, since the
+// special function unit (16 results a cycle and SM) is what bounds the scan: e = m + f with m the nearest whole
+// number, 2^f by a polynomial of degree 5 on [-1/2, 1/2] (minimax with its first two coefficients held to 1 and ln 2,
+// so that slow decays, e near zero, keep their full accuracy; relative error 1.1e-7, the special function unit's
+// 1.7e-7), m added to its exponent.  Below -126 the result is 2^-126, and so it is for NaN: a step that is NaN
+// reaches the state through its product with x.
+template <bool POLY> SELINV_DEVINL float2 decay2(float2 e)
+{
+    if constexpr (!POLY) return make_float2(exp2_(e.x), exp2_(e.y));
+    e = make_float2(fmaxf(e.x, -126.0f), fmaxf(e.y, -126.0f));
+    const float big = 12582912.0f;      // 1.5 * 2^23: the sum's low bits are the nearest whole number
+    const float2 r = add2(e, make_float2(big, big)), f = add2(e, fma2(r, make_float2(-1.0f, -1.0f), make_float2(big, big)));
+    float2 p = make_float2(0.0013300605351105332f, 0.0013300605351105332f);
+    p = fma2(p, f, make_float2(0.009669691324234009f, 0.009669691324234009f));
+    p = fma2(p, f, make_float2(0.05550558492541313f, 0.05550558492541313f));
+    p = fma2(p, f, make_float2(0.24022282660007477f, 0.24022282660007477f));
+    p = fma2(p, f, make_float2(0.6931471824645996f, 0.6931471824645996f));
+    p = fma2(p, f, make_float2(1.0f, 1.0f));
+    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(r.x) << 23)),
+                       __int_as_float(__float_as_int(p.y) + (__float_as_int(r.y) << 23)));
+}
+template <bool POLY> SELINV_DEVINL double2 decay2(double2 e) { return make_double2(exp2(e.x), exp2(e.y)); }
+
 // 1 / (1 + e^-x).
-template <class C> SELINV_DEVINL C sigmoid_(C x) { return rcp_((C)1 + exp2_(-log2e<C>() * x)); }
+SELINV_DEVINL float sigmoid_(float x) { return rcp_(1.0f + exp2_(-log2e<float>() * x)); }
 SELINV_DEVINL double sigmoid_(double x) { return 1.0 / (1.0 + exp(-x)); }
+SELINV_DEVINL float2 sigmoid2(float2 x)
+{
+    const float2 t = mul2(x, make_float2(-log2e<float>(), -log2e<float>()));
+    const float2 v = add2(make_float2(exp2_(t.x), exp2_(t.y)), make_float2(1.0f, 1.0f));
+    return make_float2(rcp_(v.x), rcp_(v.y));
+}
+SELINV_DEVINL double2 sigmoid2(double2 x) { return make_double2(sigmoid_(x.x), sigmoid_(x.y)); }
 
 // d/dx of x sigmoid(x), given p = sigmoid(x).
 template <class C> SELINV_DEVINL C silu_slope(C x, C p) { return p * ((C)1 + x * ((C)1 - p)); }
 
 // log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].  In float log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
-// by atanh's odd power series cut after s^13 (the next term is under 2^-27 of the sum): relative error of a few
-// rounding steps also for far negative x, where log(1 + e) itself would lose e's low bits.
-SELINV_DEVINL float softplus_(float x)
+// atanh(s) = s + s q r(q) with q = s^2 and r a minimax cubic on [0, 1/9] (relative error of the sum 4.5e-9): a few
+// rounding steps of relative error also for far negative x, where log(1 + e) itself would lose e's low bits.
+SELINV_DEVINL float max_nan(float a, float b)
 {
-    const float e = exp2_(-log2e<float>() * fabsf(x));
-    const float s = __fdividef(e, 2.0f + e), q = s * s;
-    float r = 1.0f / 13.0f;
-    r = fmaf(r, q, 1.0f / 11.0f);
-    r = fmaf(r, q, 1.0f / 9.0f);
-    r = fmaf(r, q, 1.0f / 7.0f);
-    r = fmaf(r, q, 1.0f / 5.0f);
-    r = fmaf(r, q, 1.0f / 3.0f);
-    r = fmaf(r * q, s, s);
-    // a NaN stays one (fmaxf alone would drop it)
-    return x == x ? fmaf(2.0f, r, fmaxf(x, 0.0f)) : x;
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
+SELINV_DEVINL float2 softplus2(float2 x)
+{
+    const float2 e = make_float2(exp2_(-log2e<float>() * fabsf(x.x)), exp2_(-log2e<float>() * fabsf(x.y)));
+    const float2 w = add2(e, make_float2(2.0f, 2.0f)), s = mul2(e, make_float2(rcp_(w.x), rcp_(w.y))), q = mul2(s, s);
+    float2 r = make_float2(0.1400599330663681f, 0.1400599330663681f);
+    r = fma2(r, q, make_float2(0.14000903069972992f, 0.14000903069972992f));
+    r = fma2(r, q, make_float2(0.2001076340675354f, 0.2001076340675354f));
+    r = fma2(r, q, make_float2(0.3333320915699005f, 0.3333320915699005f));
+    r = fma2(mul2(r, q), s, s);
+    return fma2(r, make_float2(2.0f, 2.0f), make_float2(max_nan(x.x, 0.0f), max_nan(x.y, 0.0f)));
+}
+SELINV_DEVINL float softplus_(float x) { return softplus2(make_float2(x, x)).x; }
 SELINV_DEVINL double softplus_(double x) { return x == x ? fmax(x, 0.0) + log1p(exp(-fabs(x))) : x; }
+SELINV_DEVINL double2 softplus2(double2 x) { return make_double2(softplus_(x.x), softplus_(x.y)); }
 
 // ---- reductions over lanes -------------------------------------------------
 

@@ -5,11 +5,11 @@
 
 namespace selinv {
 
-// The warp tiles of the scan: states padded to NP = 4, 8, 16, 32 or 64; `narrow` tiles hold a quarter of the
-// channels (float64 has these only, and the backward where a wide one's states do not fit).
-template <class T> int scan_tile_channels(int n, bool narrow, bool backward);
-template <class T> cudaError_t scan_launch(const ScanArgs &p, bool narrow, cudaStream_t s);
-template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, bool narrow, cudaStream_t s);
+// The warp tiles of the scan: states padded to NP = 4, 8, 16, 32 or 64; `narrow` 0, 1, 2: four, two or one states
+// per thread, and so as many more warps (float64 has one tile).  The backward takes narrow = 0.
+template <class T> int scan_tile_channels(int n, int narrow);
+template <class T> cudaError_t scan_launch(const ScanArgs &p, int narrow, cudaStream_t s);
+template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, cudaStream_t s);
 template <class T> cudaError_t scan_step_launch(const ScanStepArgs &p, cudaStream_t s);
 template <class T> cudaError_t conv_launch(const ConvArgs &p, cudaStream_t s);
 template <class T> cudaError_t conv_backward_launch(const ConvArgs &p, cudaStream_t s);
