@@ -9,7 +9,7 @@ using namespace selinv;
 
 namespace {
 
-constexpr int64_t MAX_D = 1 << 20, MAX_GRID_X = 0x7fffffff, MAX_GRID_Y = 65535;
+constexpr int64_t MAX_D = 1 << 20, MAX_ROWS = 0x7fffffff - 64, MAX_STRIDE = 0x7fffffff, MAX_GRID_X = 0x7fffffff, MAX_GRID_Y = 65535;
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -46,7 +46,7 @@ int sm_count()
     return sms;
 }
 
-bool view_ok(const selinv_view &v, size_t es) { return v.data && aligned(v.data, es) && v.line >= 0 && v.row >= 0; }
+bool view_ok(const selinv_view &v, size_t es) { return v.data && aligned(v.data, es) && v.line >= 0 && v.row >= 0 && v.row <= MAX_STRIDE; }
 
 // Whether packs of 16 bytes along the channels are aligned in every row, line and group (`group` elements apart).
 bool wide(const selinv_view &v, size_t es, int64_t group, size_t pack = 16)
@@ -55,11 +55,11 @@ bool wide(const selinv_view &v, size_t es, int64_t group, size_t pack = 16)
 }
 In in_of(const selinv_view &v, size_t es, int64_t group, size_t pack = 16)
 {
-    return In{v.data, v.line, v.row, wide(v, es, group, pack)};
+    return In{v.data, v.line, (int)v.row, wide(v, es, group, pack)};
 }
 Out out_of(const selinv_view &v, size_t es, int64_t group)
 {
-    return Out{const_cast<void *>(v.data), v.line, v.row, wide(v, es, group)};
+    return Out{const_cast<void *>(v.data), v.line, (int)v.row, wide(v, es, group)};
 }
 
 selinv_status rows_check(int64_t lines, int64_t rows, const int64_t *table, int64_t sequences, int64_t live)
@@ -68,7 +68,7 @@ selinv_status rows_check(int64_t lines, int64_t rows, const int64_t *table, int6
     if (table && (lines != 1 || sequences < 0 || live < 0 || live > sequences || live > rows || (live == 0) != (rows == 0) ||
                   !aligned(table, 8)))
         return SELINV_ERR_INVALID_ARG;
-    return SELINV_OK;
+    return rows > MAX_ROWS ? SELINV_ERR_UNSUPPORTED : SELINV_OK;
 }
 
 // ---- selective scan ----------------------------------------------------------
@@ -90,27 +90,27 @@ selinv_status scan_check(const selinv_scan_inputs &a)
     return SELINV_OK;
 }
 
-// Channels of a warp's tile.
-int64_t tile_channels(const selinv_scan_inputs &a, int narrow)
+// Channels of a warp.
+int64_t warp_channels(const selinv_scan_inputs &a, bool backward)
 {
-    return with_type(a.dtype, [&](auto t) { return scan_tile_channels<decltype(t)>((int)a.n, narrow); });
+    if (!backward) return SCAN_FORWARD_CHANNELS;
+    return with_type(a.dtype, [&](auto t) { return scan_backward_channels<decltype(t)>((int)a.n); });
 }
 
 // How a scan is spread over the GPU.
 struct Spread {
-    int narrow, segs;
-    int64_t seg_rows;
+    int segs;
+    int64_t seg_rows, tiles, blocks;        // tiles of a warp's channels and blocks of tiles, over all groups
 };
 Spread scan_spread(const selinv_scan_inputs &a, bool backward)
 {
-    const int64_t per = a.d / a.groups, want = 4 * (int64_t)sm_count();
-    const auto warps = [&](int narrow) { return a.lines * a.groups * div_up(per, tile_channels(a, narrow)); };
-    Spread s{0, 1, a.rows};
-    const int64_t w = warps(s.narrow), most = a.rows / 64 > 1 ? a.rows / 64 : 1;
-    if (w < want) {
-        const int64_t segs = div_up(2 * want, w);
-        s.segs = (int)(segs < most ? segs : most);
-    }
+    const int64_t tiles = div_up(a.d / a.groups, warp_channels(a, backward));
+    Spread s{1, a.rows, a.groups * tiles, a.groups * div_up(tiles, SCAN_BLOCK_TILES)};
+    // Lines are cut where their blocks do not fill the GPU: into so many segments that all are resident at once (four
+    // blocks per SM forward, two backward), none under 64 rows.
+    const int64_t room = (backward ? 2 : 4) * (int64_t)sm_count() / (a.lines * s.blocks > 0 ? a.lines * s.blocks : 1);
+    const int64_t most = a.rows / 64 > 1 ? a.rows / 64 : 1;
+    s.segs = (int)(room < 2 ? 1 : room < most ? room : most);
     s.seg_rows = div_up(div_up(a.rows, s.segs), SCAN_KEEP_ROWS) * SCAN_KEEP_ROWS;
     if (s.seg_rows < SCAN_KEEP_ROWS) s.seg_rows = SCAN_KEEP_ROWS;
     s.segs = (int)div_up(a.rows, s.seg_rows);
@@ -137,7 +137,7 @@ ScanSpace scan_space(const selinv_scan_inputs &a, const Spread &s, bool backward
         w.sums = take(pieces * a.d * cs);
     }
     if (backward) {
-        const size_t parts = div_up(div_up(a.d / a.groups, tile_channels(a, 0)), SCAN_BLOCK_TILES);
+        const size_t parts = s.blocks / a.groups;
         w.bc = take(parts * a.lines * a.rows * a.groups * 2 * scan_padded((int)a.n) * cs);
         w.a = take(pieces * a.d * a.n * cs);
         w.d = take(pieces * a.d * cs);
@@ -159,11 +159,9 @@ selinv_status scan_args(const selinv_scan_inputs &a, const Spread &s, ScanArgs &
 {
     const size_t es = elem(a.dtype);
     const int64_t per = a.groups > 1 ? a.d / a.groups : 0;
-    if (a.lines * s.segs > MAX_GRID_X ||
-        a.groups * div_up(div_up(a.d / a.groups, tile_channels(a, s.narrow)), SCAN_BLOCK_TILES) > MAX_GRID_Y)
-        return SELINV_ERR_UNSUPPORTED;
+    if (a.lines * s.segs > MAX_GRID_X || s.tiles > MAX_GRID_Y) return SELINV_ERR_UNSUPPORTED;
     const size_t pack = es == 2 ? 8 : 16;        // B and C: four elements at a time, two in float64
-    p.rows = Rows{a.table, a.live, a.rows};
+    p.rows = Rows{a.table, (int)a.live, (int)a.rows};
     p.lines = a.lines, p.d = a.d, p.sequences = a.sequences;
     p.n = (int)a.n, p.groups = (int)a.groups;
     p.softplus = a.flags & SELINV_SOFTPLUS;
@@ -171,7 +169,7 @@ selinv_status scan_args(const selinv_scan_inputs &a, const Spread &s, ScanArgs &
     p.B = in_of(a.B, es, a.B_group, pack), p.C = in_of(a.C, es, a.C_group, pack);
     p.B_group = a.B_group, p.C_group = a.C_group;
     p.A = a.A, p.D = a.D, p.dt_bias = a.dt_bias, p.state = a.state;
-    p.segs = s.segs, p.seg_rows = s.seg_rows;
+    p.segs = s.segs, p.seg_rows = (int)s.seg_rows;
     return SELINV_OK;
 }
 
@@ -219,13 +217,13 @@ size_t conv_space(const selinv_conv_inputs &a)
 selinv_status conv_args(const selinv_conv_inputs &a, bool backward, ConvArgs &p)
 {
     const size_t es = elem(a.dtype);
-    p.rows = Rows{a.table, a.live, a.rows};
+    p.rows = Rows{a.table, (int)a.live, (int)a.rows};
     p.lines = a.lines, p.d = a.d, p.sequences = a.sequences;
     p.k = (int)a.k;
     p.silu = a.flags & SELINV_SILU;
     p.x = in_of(a.x, es, 0);
     p.weight = a.weight, p.bias = a.bias, p.state = a.state;
-    p.chunk_rows = conv_chunk(a, backward);
+    p.chunk_rows = (int)conv_chunk(a, backward);
     const int64_t chunks = div_up(a.rows, p.chunk_rows);
     if (div_up(div_up(a.d, 16 / (int64_t)es) * a.lines * chunks, 128) > MAX_GRID_X) return SELINV_ERR_UNSUPPORTED;
     p.chunks = (int)(chunks > 1 ? chunks : 1);
@@ -264,7 +262,7 @@ selinv_status selinv_selective_scan(const selinv_scan_inputs *a, const selinv_vi
     p.y = out_of(*y, es, a->groups > 1 ? a->d / a->groups : 0);
     p.state_out = state_out, p.kept = kept;
     p.ends = static_cast<char *>(workspace) + w.ends, p.sums = static_cast<char *>(workspace) + w.sums;
-    return from_cuda(with_type(a->dtype, [&](auto t) { return scan_launch<decltype(t)>(p, spread.narrow, s); }));
+    return from_cuda(with_type(a->dtype, [&](auto t) { return scan_launch<decltype(t)>(p, s); }));
 }
 
 selinv_status selinv_selective_scan_backward(const selinv_scan_inputs *a, const selinv_scan_grads *g, void *workspace,

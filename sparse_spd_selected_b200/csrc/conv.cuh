@@ -18,8 +18,8 @@ constexpr int CONV_THREADS = 128;
 
 // A thread's chunk: line, rows [r0, r1), channels [c, c + n).
 struct ConvPlace {
-    int64_t line, r0, r1;
-    int chunk, c, n;
+    int64_t line;
+    int r0, r1, chunk, c, n;
 };
 template <int E> SELINV_DEVINL bool conv_place(const ConvArgs &p, ConvPlace &w)
 {
@@ -51,15 +51,15 @@ template <class T, int E> SELINV_DEVINL void down_row(T *p, int n, bool wide, co
 
 // The K - 1 inputs before row r of the sequence that begins at row `start`.
 template <class T, int K, int E>
-SELINV_DEVINL void conv_window(const ConvArgs &p, const T *x, int64_t start, int64_t number, int64_t r, int c, int n,
+SELINV_DEVINL void conv_window(const ConvArgs &p, const T *x, int start, int64_t number, int r, int c, int n,
                                typename Elem<T>::C (*win)[E])
 {
     const T *state = static_cast<const T *>(p.state);
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
-        const int64_t at = r - (K - 1) + i;
+        const int at = r - (K - 1) + i;
         if (at >= start) {
-            up_row<T, E>(x + at * p.x.row, n, p.x.wide, win[i]);
+            up_row<T, E>(x + (int64_t)at * p.x.row, n, p.x.wide, win[i]);
         } else if (state) {
             up_row<T, E>(state + (number * (K - 1) + (at - start + K - 1)) * p.d + c, n, false, win[i]);
         } else {
@@ -94,7 +94,7 @@ template <class T, int K> __global__ void __launch_bounds__(CONV_THREADS) conv_k
     if (state_out && p.rows.table && w.chunk == 0) {    // sequences without rows end as they began
         const T *state = static_cast<const T *>(p.state);
         for (int64_t e = 0; e < p.sequences - p.rows.live; ++e) {
-            const int64_t at = p.rows.table[2 * p.rows.live + 1 + e] * (K - 1) * p.d + w.c;
+            const int64_t at = p.rows.empty(e) * (K - 1) * p.d + w.c;
             for (int i = 0; i < K - 1; ++i)
                 for (int q = 0; q < w.n; ++q)
                     state_out[at + i * p.d + q] = state ? state[at + i * p.d + q] : Elem<T>::down((C)0);
@@ -103,14 +103,14 @@ template <class T, int K> __global__ void __launch_bounds__(CONV_THREADS) conv_k
     if (w.r0 >= w.r1) return;
     C wt[K][E], bias[E], win[K - 1 + U][E];
     conv_weights<T, K, E>(p, w, wt, bias);
-    int64_t k = p.rows.find(w.r0), end = p.rows.end(k);
+    int k = p.rows.find(w.r0), end = p.rows.end(k);
     conv_window<T, K, E>(p, x, p.rows.start(k), p.rows.number(k, w.line), w.r0, w.c, w.n, win);
-    for (int64_t r = w.r0; r < w.r1;) {
-        const int m = (int)min((int64_t)U, min(w.r1, end) - r);
+    for (int r = w.r0; r < w.r1;) {
+        const int m = min(U, min(w.r1, end) - r);
         if (m == U) {
             Pack<T, E> raw[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) raw[i].load(x + (r + i) * p.x.row, w.n, p.x.wide);
+            for (int i = 0; i < U; ++i) raw[i].load(x + (int64_t)(r + i) * p.x.row, w.n, p.x.wide);
 #pragma unroll
             for (int i = 0; i < U; ++i)
 #pragma unroll
@@ -125,7 +125,7 @@ template <class T, int K> __global__ void __launch_bounds__(CONV_THREADS) conv_k
                     for (int j = 0; j < K; ++j) v[e] += wt[j][e] * win[i + j][e];
                     if (p.silu) v[e] *= sigmoid_(v[e]);
                 }
-                down_row<T, E>(y + (r + i) * p.y.row, w.n, p.y.wide, v);
+                down_row<T, E>(y + (int64_t)(r + i) * p.y.row, w.n, p.y.wide, v);
             }
 #pragma unroll
             for (int i = 0; i < K - 1; ++i)
@@ -134,7 +134,7 @@ template <class T, int K> __global__ void __launch_bounds__(CONV_THREADS) conv_k
         } else {
             for (int i = 0; i < m; ++i) {
                 C v[E];
-                up_row<T, E>(x + (r + i) * p.x.row, w.n, p.x.wide, win[K - 1]);
+                up_row<T, E>(x + (int64_t)(r + i) * p.x.row, w.n, p.x.wide, win[K - 1]);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     v[e] = bias[e];
@@ -142,7 +142,7 @@ template <class T, int K> __global__ void __launch_bounds__(CONV_THREADS) conv_k
                     for (int j = 0; j < K; ++j) v[e] += wt[j][e] * win[j][e];
                     if (p.silu) v[e] *= sigmoid_(v[e]);
                 }
-                down_row<T, E>(y + (r + i) * p.y.row, w.n, p.y.wide, v);
+                down_row<T, E>(y + (int64_t)(r + i) * p.y.row, w.n, p.y.wide, v);
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j)
 #pragma unroll
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
     T *stateb_out = static_cast<T *>(p.stateb_out);
     if (stateb_out && p.rows.table && w.chunk == 0) {
         for (int64_t e = 0; e < p.sequences - p.rows.live; ++e) {
-            const int64_t at = p.rows.table[2 * p.rows.live + 1 + e] * (K - 1) * p.d + w.c;
+            const int64_t at = p.rows.empty(e) * (K - 1) * p.d + w.c;
             for (int i = 0; i < K - 1; ++i)
                 for (int q = 0; q < w.n; ++q)
                     stateb_out[at + i * p.d + q] = stateb ? stateb[at + i * p.d + q] : Elem<T>::down((C)0);
@@ -197,25 +197,26 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
         for (int j = 0; j < K; ++j) wsum[j][e] = 0;
     }
     if (w.r0 < w.r1) {
-        int64_t k = p.rows.find(w.r0);
-        for (int64_t r = w.r0; r < w.r1; ++k) {
-            const int64_t start = p.rows.start(k), end = p.rows.end(k), number = p.rows.number(k, w.line);
+        int k = p.rows.find(w.r0);
+        for (int r = w.r0; r < w.r1; ++k) {
+            const int start = p.rows.start(k), end = p.rows.end(k);
+            const int64_t number = p.rows.number(k, w.line);
             const bool head = start >= w.r0;                       // this chunk holds the sequence's first row
-            const int64_t m0 = head ? start - (K - 1) : w.r0, m1 = min(end, w.r1);
+            const int m0 = head ? start - (K - 1) : w.r0, m1 = min(end, w.r1);
             conv_window<T, K, E>(p, x, start, number, r, w.c, w.n, win);
 #pragma unroll
             for (int j = 0; j < K; ++j)
 #pragma unroll
                 for (int e = 0; e < E; ++e) ring[j][e] = 0;
-            for (int64_t t = r; t - (K - 1) < m1; ++t) {
+            for (int t = r; t - (K - 1) < m1; ++t) {
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j)
 #pragma unroll
                     for (int e = 0; e < E; ++e) ring[j][e] = ring[j + 1][e];
                 if (t < end) {
                     C g[E];
-                    up_row<T, E>(x + t * p.x.row, w.n, p.x.wide, win[K - 1]);
-                    up_row<T, E>(yb + t * p.yb.row, w.n, p.yb.wide, g);
+                    up_row<T, E>(x + (int64_t)t * p.x.row, w.n, p.x.wide, win[K - 1]);
+                    up_row<T, E>(yb + (int64_t)t * p.yb.row, w.n, p.yb.wide, g);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
                         if (p.silu) {
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
 #pragma unroll
                     for (int e = 0; e < E; ++e) ring[K - 1][e] = 0;
                 }
-                const int64_t m = t - (K - 1);
+                const int m = t - (K - 1);
                 if (m < m0) continue;
                 C v[E];
 #pragma unroll
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
 #pragma unroll
                     for (int j = 0; j < K; ++j) v[e] += wt[j][e] * ring[K - 1 - j][e];
                 }
-                const int64_t j = m - (end - (K - 1));             // the row of the final state that is this input
+                const int j = m - (end - (K - 1));             // the row of the final state that is this input
                 if (stateb && j >= 0) {
                     C s[E];
                     up_row<T, E>(stateb + (number * (K - 1) + j) * p.d + w.c, w.n, false, s);
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
                     for (int e = 0; e < E; ++e) v[e] += s[e];
                 }
                 if (m >= start)
-                    down_row<T, E>(xb + m * p.xb.row, w.n, p.xb.wide, v);
+                    down_row<T, E>(xb + (int64_t)m * p.xb.row, w.n, p.xb.wide, v);
                 else if (stateb_out)
                     down_row<T, E>(stateb_out + (number * (K - 1) + (m - start + K - 1)) * p.d + w.c, w.n, false, v);
             }

@@ -15,29 +15,10 @@ namespace {
 constexpr int SCAN_R = 16;
 constexpr int SCAN_WARPS = 4;
 
-// A warp's tile: TD channels x TN states in each thread, LN groups of LD lanes along the states: lane = nl * LD + dl
-// holds the channels dl * TD on and the states nl * TN on, so that the lanes that read or write shared memory together
-// lie side by side along the channels.  The same lane converts rows nl, nl + LN, ... of its channels.
-template <class T_, int TD_, int TN_, int NP_> struct ScanTile {
-    using T = T_;
-    using C = typename Elem<T>::C;
-    using V = typename Two<C>::V;
-    static constexpr int TD = TD_, TN = TN_, NP = NP_, LN = NP / TN, LD = 32 / LN, CW = LD * TD, TP = TD / 2;
-    static constexpr int PER = (SCAN_R + LN - 1) / LN;           // rows that a lane converts
-    // elements of B and C a lane converts at a time
-    static constexpr int EB = sizeof(T) == 8 ? 2 : 4, BVECS = SCAN_R * NP / EB, BPER = (BVECS + 31) / 32;
-    static_assert(LN * LD == 32 && TD * sizeof(C) == 16, "a lane's channels are 16 bytes of shared memory");
-};
-
 // Where a warp works: line and rows, channel group and channels.
 struct ScanPlace {
-    int64_t line, r0, r1;
-    int seg, group, c0, nch;     // c0: first channel (of all d); nch <= CW of them
-};
-
-template <class C> struct ScanState {
-    const C *in;        // initial states [sequences, d, n] or null
-    C *out;             // final states or null
+    int64_t line;
+    int r0, r1, seg, group, c0, nch;     // c0: first channel (of all d); nch <= CW of them
 };
 
 // Small vectors in shared memory.
@@ -107,202 +88,145 @@ template <int N> SELINV_DEVINL void put(double *p, const double2 *v)
     for (int i = 0; i < N; ++i) *reinterpret_cast<double2 *>(p + 2 * i) = v[i];
 }
 
-// A lane's rows of a tile of an array [rows, channels] (p: the lane's first channel; n of them exist).
-template <class K> struct ScanLoad {
-    using T = typename K::T;
-    Pack<T, K::TD> v[K::PER];
-    SELINV_DEVINL void load(const T *p, int64_t stride, int64_t r0, int64_t r1, int n, bool wide, int nl)
-    {
-#pragma unroll
-        for (int i = 0; i < K::PER; ++i) {
-            const int row = nl + K::LN * i;
-            v[i].clear();
-            if (row < SCAN_R && r0 + row < r1) v[i].load(p + (r0 + row) * stride, n, wide);
-        }
-    }
-};
-// The same of B or C [rows, n]: vectors of EB states, dealt out over `LANES` lanes.
-template <class K, int LANES> struct ScanLoadN {
-    using T = typename K::T;
-    static constexpr int PER = (K::BVECS + LANES - 1) / LANES;
-    Pack<T, K::EB> v[PER];
-    SELINV_DEVINL static int row(int lane, int i) { return (lane + LANES * i) / (K::NP / K::EB); }
-    SELINV_DEVINL static int first(int lane, int i) { return (lane + LANES * i) % (K::NP / K::EB) * K::EB; }
-    SELINV_DEVINL void load(const T *p, int64_t stride, int64_t r0, int64_t r1, int n, bool wide, int lane)
-    {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = row(lane, i), e = first(lane, i);
-            v[i].clear();
-            if (r < SCAN_R && r0 + r < r1) v[i].load(p + (r0 + r) * stride + e, n - e, wide);
-        }
-    }
-    // into shared memory, each value twice: a pair of equal ones for two channels
-    template <class C> SELINV_DEVINL void stage(C (*to)[2 * K::NP], int lane) const
-    {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = row(lane, i);
-            if (r >= SCAN_R) break;
-            C a[2 * K::EB];
-#pragma unroll
-            for (int e = 0; e < K::EB; ++e) a[2 * e] = a[2 * e + 1] = v[i].get(e);
-            put<2 * K::EB>(&to[r][2 * first(lane, i)], a);
-        }
-    }
-};
-
-// The thread's TD x TN part of a [d, n] array (p: the warp's first channel); what lies outside is zero.
-template <class K> SELINV_DEVINL bool part_wide(const void *p, int n, int nch)
+// Starts copying CW channels (nch of them exist) of rows r .. r1 - 1, at most SCAN_R, into `to`.
+template <int CW, class T>
+SELINV_DEVINL void raw_fetch(T (*to)[CW], const T *from, int stride, int r, int r1, int nch, bool wide, int lane)
 {
-    return n == K::NP && nch == K::CW && reinterpret_cast<uintptr_t>(p) % (K::TN * sizeof(typename K::C)) == 0;
+    constexpr int E = 16 / (int)sizeof(T), LANES = CW / E, ROWS = 32 / LANES;
+    static_assert(CW % E == 0 && LANES <= 32, "a warp copies whole rows");
+    const int nr = min(SCAN_R, r1 - r);
+    from += (int64_t)r * stride;
+    if (wide && nch == CW) {
+        const int row = lane / LANES, e = (lane % LANES) * E;
+        const T *at = from + (int64_t)row * stride + e;
+#pragma unroll
+        for (int i = 0; i < SCAN_R; i += ROWS)
+            if (row + i < nr) cp_async16(&to[row + i][e], at + (int64_t)i * stride);
+    } else {
+        for (int c = lane; c < nch; c += 32) {
+#pragma unroll 4
+            for (int i = 0; i < nr; ++i) to[i][c] = from[(int64_t)i * stride + c];
+        }
+    }
 }
-template <class K> SELINV_DEVINL void load_part(const typename K::C *p, int n, int nch, int lane, typename K::V (*v)[K::TN])
+// The next such tile into L2.
+template <int CW, class T>
+SELINV_DEVINL void raw_prefetch(const T *from, int stride, int r, int r1, int nch, int lane)
 {
-    using C = typename K::C;
-    const int d0 = (lane % K::LD) * K::TD, n0 = (lane / K::LD) * K::TN;
-    if (K::TN * sizeof(C) >= 8 && part_wide<K>(p, n, nch)) {
+    if (lane < SCAN_R && r + lane < r1 && nch > 0) prefetch_l2(from + (int64_t)(r + lane) * stride);
+}
+// The same of B or C [rows, n] into rows of NP, dealt out over THREADS threads; with zeros where states or rows are not
+// there (they take part in sums over channels).
+template <int THREADS, class T, int NP>
+SELINV_DEVINL void raw_fetch_n(T (*to)[NP], const T *from, int stride, int r, int r1, int n, bool wide, int thread)
+{
+    constexpr int E = sizeof(T) == 2 ? 4 : 16 / (int)sizeof(T), ROW = NP / E;      // 8 or 16 bytes at a time
+    const int nr = min(SCAN_R, r1 - r);
+    from += (int64_t)r * stride;
 #pragma unroll
-        for (int d = 0; d < K::TD; ++d) {
-            C t[K::TN + 1];
-            if constexpr (K::TN >= 2) get<K::TN>(p + (int64_t)(d0 + d) * n + n0, t);
+    for (int i = thread; i < SCAN_R * ROW; i += THREADS) {
+        const int row = i / ROW, e = (i % ROW) * E;
+        const T *at = from + (int64_t)row * stride + e;
+        if (wide && row < nr && e + E <= n) {
+            if constexpr (sizeof(T) == 2)
+                cp_async8(&to[row][e], at);
+            else
+                cp_async16(&to[row][e], at);
+        } else {
 #pragma unroll
-            for (int j = 0; j < K::TN; ++j) (d & 1 ? v[d / 2][j].y : v[d / 2][j].x) = t[j];
+            for (int q = 0; q < E; ++q)
+                to[row][e + q] = row < nr && e + q < n ? at[q] : Elem<T>::down((typename Elem<T>::C)0);
         }
+    }
+}
+// From there into the arithmetic type.
+template <int THREADS, class T, int NP>
+SELINV_DEVINL void raw_stage_n(typename Elem<T>::C (*to)[NP], const T (*from)[NP], int thread)
+{
+    constexpr int E = sizeof(T) == 2 ? 4 : 16 / (int)sizeof(T), ROW = NP / E;
+#pragma unroll
+    for (int i = thread; i < SCAN_R * ROW; i += THREADS) {
+        const int row = i / ROW, e = (i % ROW) * E;
+        Pack<T, E> v;
+        v.load(&from[row][e], E, true);
+        typename Elem<T>::C a[E];
+#pragma unroll
+        for (int q = 0; q < E; ++q) a[q] = v.get(q);
+        put<E>(&to[row][e], a);
+    }
+}
+
+// N states of a channel in a [d, n] array (p: the first of them, m of them exist, none where `in` is false): zero beyond;
+// in pairs.
+template <int N, class C> SELINV_DEVINL void load_states(const C *p, int m, bool in, typename Two<C>::V *v)
+{
+    if (in && m >= N && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+        C t[N];
+        get<N>(p, t);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) v[j] = make2(t[2 * j], t[2 * j + 1]);
         return;
     }
 #pragma unroll
-    for (int d = 0; d < K::TD; ++d)
-#pragma unroll
-        for (int j = 0; j < K::TN; ++j)
-            (d & 1 ? v[d / 2][j].y : v[d / 2][j].x) =
-                n0 + j < n && d0 + d < nch ? p[(int64_t)(d0 + d) * n + n0 + j] : (C)0;
+    for (int j = 0; j < N / 2; ++j)
+        v[j] = make2(in && 2 * j < m ? p[2 * j] : (C)0, in && 2 * j + 1 < m ? p[2 * j + 1] : (C)0);
 }
-template <class K> SELINV_DEVINL void store_part(typename K::C *p, int n, int nch, int lane, typename K::V (*v)[K::TN])
+template <int N, class C> SELINV_DEVINL void store_states(C *p, int m, bool in, const typename Two<C>::V *v)
 {
-    using C = typename K::C;
-    const int d0 = (lane % K::LD) * K::TD, n0 = (lane / K::LD) * K::TN;
-    if (K::TN * sizeof(C) >= 8 && part_wide<K>(p, n, nch)) {
+    if (!in) return;
+    if (m >= N && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+        C t[N];
 #pragma unroll
-        for (int d = 0; d < K::TD; ++d) {
-            C t[K::TN + 1];
-#pragma unroll
-            for (int j = 0; j < K::TN; ++j) t[j] = d & 1 ? v[d / 2][j].y : v[d / 2][j].x;
-            if constexpr (K::TN >= 2) put<K::TN>(p + (int64_t)(d0 + d) * n + n0, t);
-        }
+        for (int j = 0; j < N / 2; ++j) t[2 * j] = v[j].x, t[2 * j + 1] = v[j].y;
+        put<N>(p, t);
         return;
     }
 #pragma unroll
-    for (int d = 0; d < K::TD; ++d)
-#pragma unroll
-        for (int j = 0; j < K::TN; ++j)
-            if (n0 + j < n && d0 + d < nch)
-                p[(int64_t)(d0 + d) * n + n0 + j] = d & 1 ? v[d / 2][j].y : v[d / 2][j].x;
+    for (int j = 0; j < N / 2; ++j) {
+        if (2 * j < m) p[2 * j] = v[j].x;
+        if (2 * j + 1 < m) p[2 * j + 1] = v[j].y;
+    }
 }
-template <class K> SELINV_DEVINL void zero_part(typename K::V (*v)[K::TN])
+template <int N, class V> SELINV_DEVINL void zero_states(V *v)
 {
 #pragma unroll
-    for (int q = 0; q < K::TP; ++q)
-#pragma unroll
-        for (int j = 0; j < K::TN; ++j) v[q][j] = make2((typename K::C)0, (typename K::C)0);
-}
-// A log2 e, and whether every entry of the warp is a plain decay (finite, at most zero).
-template <class K>
-SELINV_DEVINL bool load_decay(const void *A, int64_t part, int n, int nch, int lane, typename K::V (*v)[K::TN])
-{
-    using C = typename K::C;
-    load_part<K>(static_cast<const C *>(A) + part, n, nch, lane, v);
-    bool plain = true;
-#pragma unroll
-    for (int q = 0; q < K::TP; ++q)
-#pragma unroll
-        for (int j = 0; j < K::TN; ++j) {
-            v[q][j] = mul2(v[q][j], make2(log2e<C>(), log2e<C>()));
-            plain = plain && v[q][j].x <= 0 && v[q][j].y <= 0 && v[q][j].x > -(C)1e30 && v[q][j].y > -(C)1e30;
-        }
-    return __all_sync(FULL_MASK, plain);
+    for (int j = 0; j < N / 2; ++j) v[j].x = v[j].y = 0;
 }
 
-// Which pairs of a thread's tile take their powers of two from the FMA pipe: SCAN_POLY of 8, evenly spread over the
-// pairs of four rows.
-constexpr int SCAN_POLY = 3;
-template <class K> __host__ __device__ constexpr bool poly_pair(int row, int q, int j)
+// What the segments s, s + by, ... before `to` hand on to N states of one channel (own: their place in a [d, n] array):
+// the first one's own, decayed by each later one's sum of steps and joined to that one's own.
+template <int N, class C>
+SELINV_DEVINL void scan_join(const ScanArgs &p, int64_t line, int s, int to, int by, int64_t channel, int64_t own, int m, bool in,
+                             const typename Two<C>::V *A2, typename Two<C>::V *h)
 {
-    return ((row * K::TP * K::TN + q * K::TN + j) * SCAN_POLY) % 8 + SCAN_POLY >= 8;
+    using V = typename Two<C>::V;
+    const int64_t dn = p.d * p.n;
+    const C *ends = static_cast<const C *>(p.ends) + line * p.segs * dn + own;
+    const C *sums = static_cast<const C *>(p.sums) + line * p.segs * p.d + channel;
+    load_states<N>(ends + s * dn, m, in, h);
+    for (s += by; s != to; s += by) {
+        V e[N / 2];
+        load_states<N>(ends + s * dn, m, in, e);
+        const C t = in ? sums[s * p.d] : (C)0;
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) h[j] = fma2(exp2_2(mul2(make2(t, t), A2[j])), h[j], e[j]);
+    }
 }
 
-template <class K> SELINV_DEVINL bool scan_place(const ScanArgs &p, int warp, ScanPlace &w)
+// warps of a block and channels of a warp.
+SELINV_DEVINL bool scan_place(const ScanArgs &p, int warp, int warps, int cw, ScanPlace &w)
 {
-    const int per = (int)(p.d / p.groups), tiles = (per + K::CW - 1) / K::CW;
-    const int blocks = (tiles + SCAN_WARPS - 1) / SCAN_WARPS;
+    const int per = (int)(p.d / p.groups), tiles = (per + cw - 1) / cw;
+    const int blocks = (tiles + warps - 1) / warps;
     w.line = blockIdx.x / p.segs;
     w.seg = (int)(blockIdx.x % p.segs);
     w.group = (int)blockIdx.y / blocks;
-    const int tile = ((int)blockIdx.y % blocks) * SCAN_WARPS + warp;
+    const int tile = ((int)blockIdx.y % blocks) * warps + warp;
     w.r0 = w.seg * p.seg_rows;
     w.r1 = min(p.rows.rows, w.r0 + p.seg_rows);
-    w.c0 = w.group * per + tile * K::CW;
-    w.nch = min(K::CW, per - tile * K::CW);
+    w.c0 = w.group * per + tile * cw;
+    w.nch = min(cw, per - tile * cw);
     return w.nch > 0;
-}
-
-// Channels c + 2 q and the next of an array [d] or null (zero); nd of the lane's channels exist.
-template <class K> SELINV_DEVINL typename K::V pair_of(const void *a, int64_t c, int nd, int q)
-{
-    using C = typename K::C;
-    const C *p = static_cast<const C *>(a) + c + 2 * q;
-    return make2(a && 2 * q < nd ? p[0] : (C)0, a && 2 * q + 1 < nd ? p[1] : (C)0);
-}
-
-// f(kind, q, j) for every pair of a thread's tile, `kind` telling at compile time where its power of two comes from.
-template <class K, bool POLY, int ROW, int I = 0, class F> SELINV_DEVINL void scan_pairs(F f)
-{
-    if constexpr (I < K::TP * K::TN) {
-        constexpr int q = I % K::TP, j = I / K::TP;
-        f(std::integral_constant<bool, POLY && poly_pair<K>(ROW, q, j)>(), q, j);
-        scan_pairs<K, POLY, ROW, I + 1>(f);
-    }
-}
-
-// What the segments s, s + by, ... before `to` hand on: the first one's own, decayed by each later one's sum of steps and
-// joined to that one's own.
-template <class K>
-SELINV_DEVINL void scan_join(const ScanArgs &p, const ScanPlace &w, int s, int to, int by, int lane,
-                             const typename K::V (*A2)[K::TN], typename K::V (*h)[K::TN])
-{
-    using C = typename K::C;
-    using V = typename K::V;
-    const int64_t dn = p.d * p.n, part = (int64_t)w.c0 * p.n;
-    const int d0 = (lane % K::LD) * K::TD;
-    const C *ends = static_cast<const C *>(p.ends) + w.line * p.segs * dn + part;
-    const C *sums = static_cast<const C *>(p.sums) + w.line * p.segs * p.d;
-    load_part<K>(ends + s * dn, p.n, w.nch, lane, h);
-    for (s += by; s != to; s += by) {
-        V e[K::TP][K::TN];
-        load_part<K>(ends + s * dn, p.n, w.nch, lane, e);
-#pragma unroll
-        for (int q = 0; q < K::TP; ++q) {
-            const V t = pair_of<K>(sums + s * p.d, w.c0 + d0, w.nch - d0, q);
-#pragma unroll
-            for (int j = 0; j < K::TN; ++j) h[q][j] = fma2(decay2<false>(mul2(t, A2[q][j])), h[q][j], e[q][j]);
-        }
-    }
-}
-template <class K>
-SELINV_DEVINL void scan_leave(const ScanArgs &p, const ScanPlace &w, int lane, typename K::V (*h)[K::TN], const typename K::V *total)
-{
-    using C = typename K::C;
-    const int64_t at = w.line * p.segs + w.seg;
-    const int d0 = (lane % K::LD) * K::TD;
-    store_part<K>(static_cast<C *>(p.ends) + (at * p.d + w.c0) * p.n, p.n, w.nch, lane, h);
-    if (lane / K::LD == 0) {
-        C *sums = static_cast<C *>(p.sums) + at * p.d + w.c0;
-#pragma unroll
-        for (int q = 0; q < K::TP; ++q) {
-            if (d0 + 2 * q < w.nch) sums[d0 + 2 * q] = total[q].x;
-            if (d0 + 2 * q + 1 < w.nch) sums[d0 + 2 * q + 1] = total[q].y;
-        }
-    }
 }
 
 }  // namespace

@@ -5,16 +5,17 @@
 //   xb = dt' (g . B) + D yb'        dt'b = x (g . B) + q . A     Ab = sum_t q dt'
 //   Bb = sum_d g dt' x              Cb = sum_d h yb'             Db = sum_t yb' x
 //   zb = yb silu'(z) (h . C + D x)  dtb = dt'b softplus'(dt + dt_bias).
-// A block works on SCAN_WARPS neighbouring warp tiles of channels and one
+// A thread keeps eight states (pairs in one instruction) of two channels; a
+// block works on SCAN_WARPS neighbouring warp tiles of channels and one
 // segment of a line, SCAN_R rows at a time from the end.  The states inside
 // come again from the one kept before those rows: a first run leaves every
 // SCAN_S-th in shared memory, a second one fills the registers with the
 // states and decays of SCAN_S rows, which the backward recurrence then uses
-// up.  The sums over states and over channels go through shared memory, not
-// shuffles: one store of 16 bytes per thread and row, added by the lanes that
-// finish the rows.  The sums over channels (Bb, Cb) leave a block as one
-// partial sum per row, those over rows (Ab, Db, dt_biasb) as one per segment;
-// scan_sums_kernel adds them in a fixed order.
+// up.  Sums over a channel's states end in a thread or a few lanes; those
+// over channels (Bb, Cb) go through shared memory, 16 bytes a store, and leave
+// a block as one partial sum per row; those over rows (Ab, Db, dt_biasb) leave
+// it as one per segment.  scan_sums_kernel adds the partial sums in a fixed
+// order.
 #pragma once
 
 #include "scan.cuh"
@@ -23,170 +24,201 @@ namespace selinv {
 namespace {
 
 constexpr int SCAN_S = 4;       // rows whose states and decays are in registers together
+constexpr int SCAN_P = 2;       // rows whose parts of Bb and Cb are in shared memory together
 
+// lane = nl * LD + dl holds the channels 2 dl, 2 dl + 1 and the states nl * SN on.
+template <class T_, int NP_> struct ScanBwdTile {
+    using T = T_;
+    using C = typename Elem<T>::C;
+    using V = typename Two<C>::V;
+    static constexpr int NP = NP_, SN = (NP == 4 ? 4 : 8) / (sizeof(C) / 4), KP = SN / 2, LN = NP / SN, LD = 32 / LN, CW = 2 * LD;
+    static constexpr int PER = (SCAN_R + LN - 1) / LN;          // rows whose steps and outputs a lane forms
+    static constexpr int Q = 16 / (int)sizeof(C), CHUNKS = 2 * SN / Q;      // 16 bytes of sums; B's states, then C's
+};
 template <class K> struct ScanBwdSmem {
     using C = typename K::C;
-    using V = typename K::V;
-    C dt[SCAN_R][K::CW], u[SCAN_R][K::CW], yb[SCAN_R][K::CW];
-    C gb[SCAN_S][K::LN][K::CW], qa[SCAN_S][K::LN][K::CW], hc[SCAN_S][K::LN][K::CW];     // parts of the sums over states
-    C part[SCAN_S][K::LN][2 * K::TN / K::TD][K::LD][K::TD];     // parts of the sums over channels: B's states, then C's
-    C bc[SCAN_R][2 * K::NP];                                    // those sums of this warp
-    V h[SCAN_R / SCAN_S - 1][K::TP * K::TN][32];                // states before rows SCAN_S, 2 SCAN_S, ...
+    using T = typename K::T;
+    alignas(16) T x[SCAN_R][K::CW], dt_raw[SCAN_R][K::CW], z[SCAN_R][K::CW], yb_raw[SCAN_R][K::CW];
+    alignas(16) C dt[SCAN_R][K::CW], yb[SCAN_R][K::CW], gb[SCAN_R][K::CW], qa[SCAN_R][K::CW], hc[SCAN_R][K::CW];
+    alignas(16) C part[SCAN_P][K::LN][K::CHUNKS][K::LD][K::Q];
+    alignas(16) C bc[SCAN_R][2 * K::NP];
+    alignas(16) typename K::V h[SCAN_R / SCAN_S - 1][2 * K::KP][32];    // states before rows SCAN_S, 2 SCAN_S, ...
 };
 template <class K> struct ScanBwdBlock {
     using C = typename K::C;
+    using T = typename K::T;
     ScanBwdSmem<K> warp[SCAN_WARPS];
-    C b[SCAN_R][2 * K::NP], c[SCAN_R][2 * K::NP];
+    alignas(16) T b_raw[SCAN_R][K::NP], c_raw[SCAN_R][K::NP];
+    alignas(16) C b[SCAN_R][K::NP], c[SCAN_R][K::NP];
 };
-
-// a and h of row t.
-template <class K, bool POLY, int ROW>
-SELINV_DEVINL void scan_again(const ScanBwdSmem<K> &sm, const ScanBwdBlock<K> &block, int t, int d0, int n0, int n,
-                              const typename K::V (*A2)[K::TN], typename K::V (*h)[K::TN], typename K::V (*a)[K::TN])
-{
-    using V = typename K::V;
-    using C = typename K::C;
-    V dt2[K::TP], u2[K::TP], b2[K::TN];
-    get<K::TP>(&sm.dt[t][d0], dt2);
-    get<K::TP>(&sm.u[t][d0], u2);
-    get<K::TN>(&block.b[t][2 * n0], b2);
-    scan_pairs<K, POLY, ROW>([&](auto poly, int q, int j) {
-        a[q][j] = decay2<poly.value>(mul2(dt2[q], A2[q][j]));
-        h[q][j] = fma2(a[q][j], h[q][j], mul2(u2[q], b2[j]));
-    });
-    if (n < K::NP) {
-#pragma unroll
-        for (int j = 0; j < K::TN; ++j)
-            if (n0 + j >= n) {
-#pragma unroll
-                for (int q = 0; q < K::TP; ++q) h[q][j] = make2((C)0, (C)0);
-            }
-    }
-}
 
 // What a thread of the backward knows of its place.
 template <class K> struct ScanBwd {
     using T = typename K::T;
     using C = typename K::C;
     using V = typename K::V;
+    static constexpr int KP = K::KP, SN = K::SN;
     const ScanArgs &p;
     const ScanGrads &o;
     ScanBwdBlock<K> &block;
     ScanBwdSmem<K> &sm;
-    int lane, nl, d0, n0, nch;
-    int64_t line, part, dn;         // part: the warp's first channel in a [d, n] array
+    int lane, nl, c, n0, nch;       // c: the first of the two channels, among the warp's
+    int64_t line, part, dn;         // part: that channel's place in a [d, n] array
 
-    SELINV_DEVINL void states(const void *from, int64_t sequence, V (*v)[K::TN]) const
+    SELINV_DEVINL void load(const C *from, V (*v)[KP]) const
     {
-        if (from)
-            load_part<K>(static_cast<const C *>(from) + p.rows.number(sequence, line) * dn + part, p.n, nch, lane, v);
-        else
-            zero_part<K>(v);
+        load_states<SN>(from + part + n0, p.n - n0, c < nch, v[0]);
+        load_states<SN>(from + part + p.n + n0, p.n - n0, c + 1 < nch, v[1]);
+    }
+    SELINV_DEVINL void store(C *to, const V (*v)[KP]) const
+    {
+        store_states<SN>(to + part + n0, p.n - n0, c < nch, v[0]);
+        store_states<SN>(to + part + p.n + n0, p.n - n0, c + 1 < nch, v[1]);
+    }
+    SELINV_DEVINL void states(const void *from, int sequence, V (*v)[KP]) const
+    {
+        if (from) {
+            load(static_cast<const C *>(from) + p.rows.number(sequence, line) * dn, v);
+        } else {
+            zero_states<SN>(v[0]);
+            zero_states<SN>(v[1]);
+        }
     }
     // The live sequence of row t of a tile whose first row lies in k0; st: the rows that begin one.
-    SELINV_DEVINL static int64_t sequence(int64_t k0, uint32_t st, int t) { return k0 + __popc(st & ((2u << t) - 2u)); }
+    SELINV_DEVINL static int sequence(int k0, uint32_t st, int t) { return k0 + __popc(st & ((2u << t) - 2u)); }
 
+    // dt' and x of the two channels of row t
+    SELINV_DEVINL void inputs(int t, V &dt, V &x) const
+    {
+        dt = *reinterpret_cast<const V *>(&sm.dt[t][c]);
+        Pack<T, 2> v;
+        v.load(&sm.x[t][c], 2, true);
+        x = make2(v.get(0), v.get(1));
+    }
+    // Row t: the state before it becomes the state after it; its decays.
+    SELINV_DEVINL void row(int t, const V (*A2)[KP], V (*h)[KP], V (*a)[KP]) const
+    {
+        V dt, x, b[KP];
+        inputs(t, dt, x);
+        get<KP>(&block.b[t][n0], b);
+        const V u = mul2(dt, x), d0 = make2(dt.x, dt.x), d1 = make2(dt.y, dt.y), u0 = make2(u.x, u.x), u1 = make2(u.y, u.y);
+#pragma unroll
+        for (int j = 0; j < KP; ++j) {
+            a[0][j] = exp2_2(mul2(d0, A2[0][j]));
+            a[1][j] = exp2_2(mul2(d1, A2[1][j]));
+            h[0][j] = fma2(a[0][j], h[0][j], mul2(u0, b[j]));
+            h[1][j] = fma2(a[1][j], h[1][j], mul2(u1, b[j]));
+        }
+    }
+    // SCAN_S rows of the first run.  EDGE: some row begins a sequence.
+    template <bool EDGE> SELINV_DEVINL void skip(int t0, uint32_t begins, int k0, const V (*A2)[KP], V (*h)[KP]) const
+    {
+#pragma unroll
+        for (int r = 0; r < SCAN_S; ++r) {
+            V a[2][KP];
+            if (EDGE && ((begins >> (t0 + r)) & 1u)) states(p.state, sequence(k0, begins, t0 + r), h);
+            row(t0 + r, A2, h, a);
+        }
+    }
     // Rows t0 .. t0 + SCAN_S - 1, `before` the state before them.  EDGE: some row begins or ends a sequence; st has the
     // rows that begin one and the row behind the last, of which only those below nr are rows.
-    template <bool POLY, bool EDGE>
-    SELINV_DEVINL void rows(int t0, int nr, uint32_t st, int64_t k0, const V (*A2)[K::TN], const V (*before)[K::TN], V (*g)[K::TN],
-                            V (*ab)[K::TN]) const
+    template <bool EDGE>
+    SELINV_DEVINL void rows(int t0, int nr, uint32_t st, int k0, const V (*A2)[KP], const V (*before)[KP], V (*g)[KP],
+                            V (*ab)[KP]) const
     {
-        constexpr int S = SCAN_S, TP = K::TP, TN = K::TN;
-        V h[S][TP][TN], a[S][TP][TN];
+        constexpr int S = SCAN_S;
         const uint32_t begins = st & ((1u << nr) - 1u);
-        run<POLY, EDGE, 0>(t0, begins, k0, A2, before, h, a);
+        V h[S][2][KP], a[S][2][KP];
+#pragma unroll
+        for (int r = 0; r < S; ++r) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < KP; ++j) h[r][i][j] = r ? h[r ? r - 1 : 0][i][j] : before[i][j];
+            if (EDGE && ((begins >> (t0 + r)) & 1u)) states(p.state, sequence(k0, begins, t0 + r), h[r]);
+            row(t0 + r, A2, h[r], a[r]);
+        }
 #pragma unroll
         for (int r = S - 1; r >= 0; --r) {
             const int t = t0 + r;
             if (EDGE && ((st >> (t + 1)) & 1u)) states(o.stateb, sequence(k0, st, t), g);
             const bool first = EDGE && ((begins >> t) & 1u);
-            V start[TP][TN];
+            V start[2][KP];
             if (EDGE) {
                 if (first) {
                     states(p.state, sequence(k0, st, t), start);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < TP; ++q)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int j = 0; j < TN; ++j) start[q][j] = r > 0 ? h[r > 0 ? r - 1 : 0][q][j] : before[q][j];
+                        for (int j = 0; j < KP; ++j) start[i][j] = r > 0 ? h[r > 0 ? r - 1 : 0][i][j] : before[i][j];
                 }
             }
-            V dt2[TP], u2[TP], yb2[TP], b2[TN], c2[TN], gb[TP], qa[TP];
-            get<TP>(&sm.dt[t][d0], dt2);
-            get<TP>(&sm.u[t][d0], u2);
-            get<TP>(&sm.yb[t][d0], yb2);
-            get<TN>(&block.b[t][2 * n0], b2);
-            get<TN>(&block.c[t][2 * n0], c2);
-            C sum[2 * TN];
+            V dt, x, b[KP], c2[KP], gb[2], qa[2], hc[2], sb[KP], sc[KP];
+            inputs(t, dt, x);
+            const V yb = *reinterpret_cast<const V *>(&sm.yb[t][c]), u = mul2(dt, x);
+            get<KP>(&block.b[t][n0], b);
+            get<KP>(&block.c[t][n0], c2);
+            const V d2[2] = {make2(dt.x, dt.x), make2(dt.y, dt.y)}, u2[2] = {make2(u.x, u.x), make2(u.y, u.y)};
+            const V y2[2] = {make2(yb.x, yb.x), make2(yb.y, yb.y)};
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                V sb, sc;
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int q = 0; q < TP; ++q) {
-                    const V past = EDGE ? start[q][j] : r > 0 ? h[r > 0 ? r - 1 : 0][q][j] : before[q][j];
-                    const V gt = fma2(c2[j], yb2[q], g[q][j]);
-                    sb = q ? fma2(gt, u2[q], sb) : mul2(gt, u2[q]);
-                    sc = q ? fma2(h[r][q][j], yb2[q], sc) : mul2(h[r][q][j], yb2[q]);
-                    gb[q] = j ? fma2(gt, b2[j], gb[q]) : mul2(gt, b2[j]);
-                    g[q][j] = mul2(a[r][q][j], gt);
-                    const V m = mul2(g[q][j], past);
-                    qa[q] = j ? fma2(m, A2[q][j], qa[q]) : mul2(m, A2[q][j]);
-                    ab[q][j] = fma2(m, dt2[q], ab[q][j]);
+                for (int j = 0; j < KP; ++j) {
+                    const V past = EDGE ? start[i][j] : r > 0 ? h[r > 0 ? r - 1 : 0][i][j] : before[i][j];
+                    const V gt = fma2(c2[j], y2[i], g[i][j]);
+                    sb[j] = i ? fma2(gt, u2[i], sb[j]) : mul2(gt, u2[i]);
+                    sc[j] = i ? fma2(h[r][i][j], y2[i], sc[j]) : mul2(h[r][i][j], y2[i]);
+                    gb[i] = j ? fma2(gt, b[j], gb[i]) : mul2(gt, b[j]);
+                    hc[i] = j ? fma2(h[r][i][j], c2[j], hc[i]) : mul2(h[r][i][j], c2[j]);
+                    g[i][j] = mul2(a[r][i][j], gt);
+                    const V m = mul2(g[i][j], past);
+                    qa[i] = j ? fma2(m, A2[i][j], qa[i]) : mul2(m, A2[i][j]);
+                    ab[i][j] = fma2(m, d2[i], ab[i][j]);
                 }
-                sum[j] = sb.x + sb.y, sum[TN + j] = sc.x + sc.y;
             }
-            if (p.n < K::NP) {
+            C v[3][2];
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    if (n0 + j >= p.n) {
+            for (int i = 0; i < 2; ++i) v[0][i] = gb[i].x + gb[i].y, v[1][i] = qa[i].x + qa[i].y, v[2][i] = hc[i].x + hc[i].y;
 #pragma unroll
-                        for (int q = 0; q < TP; ++q) g[q][j] = make2((C)0, (C)0);
-                    }
+            for (int e = 0; e < 3; ++e) scatter_sum<2, K::LD, 32>(v[e], lane);
+            constexpr int KEEP = K::LN == 1 ? 2 : 1;
+            if (scatter_writes<2, K::LD, 32>(lane)) {
+                const int f = c + scatter_first<2, K::LD, 32>(lane);
+#pragma unroll
+                for (int i = 0; i < KEEP; ++i) sm.gb[t][f + i] = v[0][i], sm.qa[t][f + i] = v[1][i], sm.hc[t][f + i] = v[2][i];
             }
-            put<TP>(&sm.gb[r][nl][d0], gb);
-            put<TP>(&sm.qa[r][nl][d0], qa);
-            if (p.z.p) {
-                V hc[TP];
+            C out[2 * SN];
 #pragma unroll
-                for (int q = 0; q < TP; ++q) {
-                    hc[q] = mul2(c2[0], h[r][q][0]);
-#pragma unroll
-                    for (int j = 1; j < TN; ++j) hc[q] = fma2(c2[j], h[r][q][j], hc[q]);
-                }
-                put<TP>(&sm.hc[r][nl][d0], hc);
+            for (int j = 0; j < KP; ++j) {
+                out[2 * j] = sb[j].x, out[2 * j + 1] = sb[j].y;
+                out[SN + 2 * j] = sc[j].x, out[SN + 2 * j + 1] = sc[j].y;
             }
 #pragma unroll
-            for (int i = 0; i < 2 * TN / K::TD; ++i) put<K::TD>(&sm.part[r][nl][i][lane % K::LD][0], sum + i * K::TD);
-            if (first && o.stateb_out)
-                store_part<K>(static_cast<C *>(o.stateb_out) + p.rows.number(sequence(k0, st, t), line) * dn + part, p.n, nch,
-                              lane, g);
+            for (int i = 0; i < K::CHUNKS; ++i) put<K::Q>(&sm.part[r % SCAN_P][nl][i][lane % K::LD][0], out + i * K::Q);
+            if (first && o.stateb_out) store(static_cast<C *>(o.stateb_out) + p.rows.number(sequence(k0, st, t), line) * dn, g);
+            if (r % SCAN_P == 0) {
+                __syncwarp();
+                sums(t);
+                __syncwarp();
+            }
         }
     }
-    // The states and decays of rows t0 + R on.
-    template <bool POLY, bool EDGE, int R>
-    SELINV_DEVINL void run(int t0, uint32_t st, int64_t k0, const V (*A2)[K::TN], const V (*before)[K::TN],
-                           V (*h)[K::TP][K::TN], V (*a)[K::TP][K::TN]) const
+    // Bb's and Cb's sums over this warp's channels for rows t .. t + SCAN_P - 1: a pair of states at a time, from another
+    // lane's part on each, so that the lanes read other banks.
+    SELINV_DEVINL void sums(int t) const
     {
-        if constexpr (R < SCAN_S) {
+        constexpr int HALVES = K::Q / 2, PAIRS = K::LN * K::CHUNKS * HALVES;
 #pragma unroll
-            for (int q = 0; q < K::TP; ++q)
+        for (int i = lane; i < SCAN_P * PAIRS; i += 32) {
+            const int r = i / PAIRS, pair = i % PAIRS, half = pair % HALVES, chunk = pair / HALVES;
+            const int m = chunk / K::CHUNKS, ch = chunk % K::CHUNKS;
+            V v = *reinterpret_cast<const V *>(&sm.part[r][m][ch][chunk % K::LD][2 * half]);
 #pragma unroll
-                for (int j = 0; j < K::TN; ++j) h[R][q][j] = R ? h[R ? R - 1 : 0][q][j] : before[q][j];
-            if (EDGE && ((st >> (t0 + R)) & 1u)) states(p.state, sequence(k0, st, t0 + R), h[R]);
-            scan_again<K, POLY, R>(sm, block, t0 + R, d0, n0, p.n, A2, h[R], a[R]);
-            run<POLY, EDGE, R + 1>(t0, st, k0, A2, before, h, a);
-        }
-    }
-    // SCAN_S rows of the first run.
-    template <bool POLY, bool EDGE, int R = 0>
-    SELINV_DEVINL void skip(int t0, uint32_t st, int64_t k0, const V (*A2)[K::TN], V (*h)[K::TN]) const
-    {
-        if constexpr (R < SCAN_S) {
-            V a[K::TP][K::TN];
-            if (EDGE && ((st >> (t0 + R)) & 1u)) states(p.state, sequence(k0, st, t0 + R), h);
-            scan_again<K, POLY, R>(sm, block, t0 + R, d0, n0, p.n, A2, h, a);
-            skip<POLY, EDGE, R + 1>(t0, st, k0, A2, h);
+            for (int f = 1; f < K::LD; ++f)
+                v = add2(v, *reinterpret_cast<const V *>(&sm.part[r][m][ch][(chunk + f) % K::LD][2 * half]));
+            const int j = ch * K::Q + 2 * half;         // among B's states and then C's of lane group m
+            *reinterpret_cast<V *>(&sm.bc[t + r][(j / SN) * K::NP + m * SN + j % SN]) = v;
         }
     }
 };
@@ -198,358 +230,338 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
     using T = typename K::T;
     using C = typename K::C;
     using V = typename K::V;
-    constexpr int R = SCAN_R, S = SCAN_S, LN = K::LN, LD = K::LD, NP = K::NP, TD = K::TD, TN = K::TN, TP = K::TP;
-    constexpr int PERS = S > LN ? S / LN : 1;       // rows of S that a lane finishes
+    constexpr int R = SCAN_R, S = SCAN_S, LN = K::LN, LD = K::LD, NP = K::NP, SN = K::SN, KP = K::KP, CW = K::CW, PER = K::PER;
     extern __shared__ __align__(16) char smem_raw[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     ScanBwdBlock<K> &block = *reinterpret_cast<ScanBwdBlock<K> *>(smem_raw);
     ScanBwdSmem<K> &sm = block.warp[warp];
     ScanPlace w;
-    scan_place<K>(p, warp, w);              // a warp without channels (nch <= 0) still meets the others
+    scan_place(p, warp, SCAN_WARPS, CW, w);     // a warp without channels (nch <= 0) still meets the others
     w.nch = max(w.nch, 0);
-    if (w.nch == 0) w.c0 = 0;               // its addresses are never used
+    if (w.nch == 0) w.c0 = 0;                   // its addresses are never used
 
-    const int n = p.n, nl = lane / LD, d0 = (lane % LD) * TD, n0 = nl * TN, nd = w.nch - d0;
-    const T *x = static_cast<const T *>(p.x.p) + w.line * p.x.line + w.c0 + d0;
-    const T *dt = static_cast<const T *>(p.dt.p) + w.line * p.dt.line + w.c0 + d0;
-    const T *z = p.z.p ? static_cast<const T *>(p.z.p) + w.line * p.z.line + w.c0 + d0 : nullptr;
+    const int n = p.n, nl = lane / LD, c = 2 * (lane % LD), n0 = nl * SN;
+    const T *x = static_cast<const T *>(p.x.p) + w.line * p.x.line + w.c0;
+    const T *dt = static_cast<const T *>(p.dt.p) + w.line * p.dt.line + w.c0;
+    const T *z = p.z.p ? static_cast<const T *>(p.z.p) + w.line * p.z.line + w.c0 : nullptr;
     const T *B = static_cast<const T *>(p.B.p) + w.line * p.B.line + w.group * p.B_group;
     const T *Cc = static_cast<const T *>(p.C.p) + w.line * p.C.line + w.group * p.C_group;
-    const T *yb = static_cast<const T *>(o.yb.p) + w.line * o.yb.line + w.c0 + d0;
-    T *xb = static_cast<T *>(o.xb.p) + w.line * o.xb.line + w.c0 + d0;
-    T *dtb = static_cast<T *>(o.dtb.p) + w.line * o.dtb.line + w.c0 + d0;
-    T *zb = o.zb.p ? static_cast<T *>(o.zb.p) + w.line * o.zb.line + w.c0 + d0 : nullptr;
-    const int64_t part = (int64_t)w.c0 * n, dn = p.d * n;
-    const ScanBwd<K> at{p, o, block, sm, lane, nl, d0, n0, w.nch, w.line, part, dn};
+    const T *yb = static_cast<const T *>(o.yb.p) + w.line * o.yb.line + w.c0;
+    T *xb = static_cast<T *>(o.xb.p) + w.line * o.xb.line + w.c0 + c;
+    T *dtb = static_cast<T *>(o.dtb.p) + w.line * o.dtb.line + w.c0 + c;
+    T *zb = o.zb.p ? static_cast<T *>(o.zb.p) + w.line * o.zb.line + w.c0 + c : nullptr;
+    const int64_t dn = p.d * n, part = (int64_t)(w.c0 + c) * n;
+    const ScanBwd<K> at{p, o, block, sm, lane, nl, c, n0, w.nch, w.line, part, dn};
 
-    if (o.stateb_out && p.rows.table && blockIdx.x == 0) {      // sequences without rows
+    if (o.stateb_out && p.rows.table && blockIdx.x == 0 && nl == 0) {       // sequences without rows
         C *out = static_cast<C *>(o.stateb_out);
         const C *in = static_cast<const C *>(o.stateb);
         for (int64_t e = 0; e < p.sequences - p.rows.live; ++e) {
-            const int64_t a = p.rows.table[2 * p.rows.live + 1 + e] * dn + part;
-            for (int i = lane; i < w.nch * n; i += 32) out[a + i] = in ? in[a + i] : (C)0;
+            const int64_t a = p.rows.empty(e) * dn + part;
+            for (int i = 0; i < n * min(2, w.nch - c); ++i) out[a + i] = in ? in[a + i] : (C)0;
         }
     }
 
-    V A2[TP][TN], g[TP][TN], ab[TP][TN];       // g: what the row behind hands on, a_{t+1} g_{t+1}
-    V bias[TP], skip[TP], sum_d[TP], sum_bias[TP];
-    const bool plain = load_decay<K>(p.A, part, n, w.nch, lane, A2) && p.softplus;
-    zero_part<K>(g);
-    zero_part<K>(ab);
+    V A2[2][KP], g[2][KP], ab[2][KP];       // g: what the row behind hands on, a_{t+1} g_{t+1}
+    at.load(static_cast<const C *>(p.A), A2);
+    C bias[2], skip[2];
+    V sum_d = make2((C)0, (C)0), sum_bias = sum_d;
 #pragma unroll
-    for (int q = 0; q < TP; ++q) {
-        bias[q] = pair_of<K>(p.dt_bias, w.c0 + d0, nd, q);
-        skip[q] = pair_of<K>(p.D, w.c0 + d0, nd, q);
-        sum_d[q] = sum_bias[q] = make2((C)0, (C)0);
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < KP; ++j) A2[i][j] = mul2(A2[i][j], make2(log2e<C>(), log2e<C>()));
+        zero_states<SN>(g[i]);
+        zero_states<SN>(ab[i]);
+        bias[i] = c + i < w.nch && p.dt_bias ? static_cast<const C *>(p.dt_bias)[w.c0 + c + i] : (C)0;
+        skip[i] = c + i < w.nch && p.D ? static_cast<const C *>(p.D)[w.c0 + c + i] : (C)0;
     }
-    int64_t k0 = w.r1 > w.r0 ? p.rows.find(w.r1 - 1) : 0;
-    if (w.r1 > w.r0 && p.rows.end(k0) > w.r1)       // what the segments behind this one hand on
-        scan_join<K>(p, w, (int)((p.rows.end(k0) - 1) / p.seg_rows), w.seg, -1, lane, A2, g);
-    const int64_t tiles = (p.rows.rows + R - 1) / R;
-    const int per = (int)(p.d / p.groups), tiles_c = (per + K::CW - 1) / K::CW;
+    int k0 = w.r1 > w.r0 ? p.rows.find(w.r1 - 1) : 0;
+    if (w.r1 > w.r0 && p.rows.end(k0) > w.r1) {         // what the segments behind this one hand on
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            scan_join<SN, C>(p, w.line, (p.rows.end(k0) - 1) / p.seg_rows, w.seg, -1, w.c0 + c + i, part + i * n + n0, n - n0,
+                             c + i < w.nch, A2[i], g[i]);
+    }
+    const int tiles = (p.rows.rows + R - 1) / R;
+    const int per = (int)(p.d / p.groups), tiles_c = (per + CW - 1) / CW;
     const int blocks = (tiles_c + SCAN_WARPS - 1) / SCAN_WARPS, bi = (int)blockIdx.y % blocks;
     const int live = min(SCAN_WARPS, tiles_c - bi * SCAN_WARPS);
     C *part_bc = static_cast<C *>(o.part_bc) +
                  (((int64_t)bi * p.lines + w.line) * p.rows.rows * p.groups + w.group) * 2 * NP;
+    const bool out_wide = o.xb.wide && o.dtb.wide && (!z || o.zb.wide);
 
-    for (int64_t rt = w.r0 + (w.r1 > w.r0 ? (w.r1 - w.r0 - 1) / R * R : 0); rt >= w.r0 && rt < w.r1; rt -= R) {
-        const int nr = (int)min((int64_t)R, w.r1 - rt);
+    auto fetch = [&](int r) {
+        raw_fetch<CW>(sm.x, x, p.x.row, r, w.r1, w.nch, p.x.wide, lane);
+        raw_fetch<CW>(sm.dt_raw, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
+        raw_fetch<CW>(sm.yb_raw, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
+        if (z) raw_fetch<CW>(sm.z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
+        raw_fetch_n<SCAN_WARPS * 32>(block.b_raw, B, p.B.row, r, w.r1, n, p.B.wide, threadIdx.x);
+        raw_fetch_n<SCAN_WARPS * 32>(block.c_raw, Cc, p.C.row, r, w.r1, n, p.C.wide, threadIdx.x);
+        cp_async_commit();
+    };
+    int rt = w.r0 + (w.r1 > w.r0 ? (w.r1 - w.r0 - 1) / R * R : 0);
+    if (w.r1 > w.r0) fetch(rt);
+    for (; rt >= w.r0 && rt < w.r1; rt -= R) {
+        const int nr = min(R, w.r1 - rt);
         while (p.rows.start(k0) > rt) --k0;         // the live sequence of this tile's first row
-        const uint32_t st = p.rows.starts(rt, R, k0, lane);
-        // stage; rows that are not there (behind the last) change nothing: no step, no input, no cotangent
-        {
-            ScanLoad<K> xl, dl, yl, zl;
-            ScanLoadN<K, SCAN_WARPS * 32> bl, cl;
-            dl.load(dt, p.dt.row, rt, w.r1, nd, p.dt.wide, nl);
-            xl.load(x, p.x.row, rt, w.r1, nd, p.x.wide, nl);
-            yl.load(yb, o.yb.row, rt, w.r1, nd, o.yb.wide, nl);
-            if (z) zl.load(z, p.z.row, rt, w.r1, nd, p.z.wide, nl);
-            bl.load(B, p.B.row, rt, w.r1, n, p.B.wide, threadIdx.x);
-            cl.load(Cc, p.C.row, rt, w.r1, n, p.C.wide, threadIdx.x);
+        const uint32_t st = p.rows.starts(rt, R, k0, lane), begins = st & ((1u << nr) - 1u);
+        cp_async_wait_all();
+        __syncthreads();
+        raw_stage_n<SCAN_WARPS * 32>(block.b, block.b_raw, threadIdx.x);
+        raw_stage_n<SCAN_WARPS * 32>(block.c, block.c_raw, threadIdx.x);
+        if (rt > w.r0) {
+            raw_prefetch<CW>(x, p.x.row, rt - R, w.r1, w.nch, lane);
+            raw_prefetch<CW>(dt, p.dt.row, rt - R, w.r1, w.nch, lane);
+            raw_prefetch<CW>(yb, o.yb.row, rt - R, w.r1, w.nch, lane);
+            if (z) raw_prefetch<CW>(z, p.z.row, rt - R, w.r1, w.nch, lane);
+        }
+        {       // steps and gated cotangents; rows and channels that are not there have no step, no input, no cotangent
+            V a[PER], y[PER];
 #pragma unroll
-            for (int i = 0; i < K::PER; ++i) {
+            for (int i = 0; i < PER; ++i) {
+                const int row = min(nl + LN * i, R - 1);
+                Pack<T, 2> v;
+                v.load(&sm.dt_raw[row][c], 2, true);
+                a[i] = make2(v.get(0) + bias[0], v.get(1) + bias[1]);
+                v.load(&sm.yb_raw[row][c], 2, true);
+                y[i] = make2(v.get(0), v.get(1));
+            }
+            if (p.softplus) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) a[i] = softplus2(a[i]);
+            }
+            if (z) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    Pack<T, 2> v;
+                    v.load(&sm.z[min(nl + LN * i, R - 1)][c], 2, true);
+                    const V q = make2(v.get(0), v.get(1));
+                    y[i] = mul2(y[i], mul2(q, sigmoid2(q)));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
                 const int row = nl + LN * i;
                 if (row >= R) break;
-                V a[TP], b[TP], c[TP];
-#pragma unroll
-                for (int q = 0; q < TP; ++q) {
-                    a[q] = add2(make2(dl.v[i].get(2 * q), dl.v[i].get(2 * q + 1)), bias[q]);
-                    if (p.softplus) a[q] = softplus2(a[q]);
-                    if (row >= nr) a[q] = make2((C)0, (C)0);
-                    b[q] = mul2(a[q], make2(xl.v[i].get(2 * q), xl.v[i].get(2 * q + 1)));
-                    c[q] = make2(yl.v[i].get(2 * q), yl.v[i].get(2 * q + 1));
-                    if (z) {
-                        const V v = make2(zl.v[i].get(2 * q), zl.v[i].get(2 * q + 1));
-                        c[q] = mul2(c[q], mul2(v, sigmoid2(v)));
-                    }
-                }
-                put<TP>(&sm.dt[row][d0], a);
-                put<TP>(&sm.u[row][d0], b);
-                put<TP>(&sm.yb[row][d0], c);
+                const bool in0 = row < nr && c < w.nch, in1 = row < nr && c + 1 < w.nch;
+                *reinterpret_cast<V *>(&sm.dt[row][c]) = make2(in0 ? a[i].x : (C)0, in1 ? a[i].y : (C)0);
+                *reinterpret_cast<V *>(&sm.yb[row][c]) = make2(in0 ? y[i].x : (C)0, in1 ? y[i].y : (C)0);
+                if (!in0) sm.x[row][c] = Elem<T>::down((C)0);
+                if (!in1) sm.x[row][c + 1] = Elem<T>::down((C)0);
             }
-            bl.stage(block.b, threadIdx.x);
-            cl.stage(block.c, threadIdx.x);
         }
         __syncthreads();
 
-        V h[TP][TN];
-        const C *kept = static_cast<const C *>(o.kept) + (w.line * tiles + rt / R) * dn + part;
-        load_part<K>(kept, n, w.nch, lane, h);
+        V h[2][KP];
+        const C *kept = static_cast<const C *>(o.kept) + (w.line * tiles + rt / R) * dn;
+        at.load(kept, h);
         for (int b = 0; b < R / S - 1 && (b + 1) * S < nr; ++b) {
-            if ((st >> (b * S)) & ((1u << S) - 1u))
-                at.template skip<false, true>(b * S, st, k0, A2, h);
-            else if (plain)
-                at.template skip<true, false>(b * S, st, k0, A2, h);
+            if ((begins >> (b * S)) & ((1u << S) - 1u))
+                at.template skip<true>(b * S, begins, k0, A2, h);
             else
-                at.template skip<false, false>(b * S, st, k0, A2, h);
+                at.template skip<false>(b * S, begins, k0, A2, h);
 #pragma unroll
-            for (int q = 0; q < TP; ++q)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) sm.h[b][q * TN + j][lane] = h[q][j];
+                for (int j = 0; j < KP; ++j) sm.h[b][i * KP + j][lane] = h[i][j];
         }
         for (int b = (nr - 1) / S; b >= 0; --b) {
-            const int t0 = b * S;
             if (b > 0) {
 #pragma unroll
-                for (int q = 0; q < TP; ++q)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int j = 0; j < TN; ++j) h[q][j] = sm.h[b - 1][q * TN + j][lane];
+                    for (int j = 0; j < KP; ++j) h[i][j] = sm.h[b - 1][i * KP + j][lane];
             } else {
-                load_part<K>(kept, n, w.nch, lane, h);
+                at.load(kept, h);
             }
-            Pack<T, TD> xv[PERS], dv[PERS], yv[PERS], zv[PERS];
-#pragma unroll
-            for (int i = 0; i < PERS; ++i) {
-                const int row = t0 + nl + LN * i;
-                xv[i].clear(), dv[i].clear(), yv[i].clear(), zv[i].clear();
-                if (nl < S && row < nr) {
-                    xv[i].load(x + (rt + row) * p.x.row, nd, p.x.wide);
-                    dv[i].load(dt + (rt + row) * p.dt.row, nd, p.dt.wide);
-                    if (z) {
-                        yv[i].load(yb + (rt + row) * o.yb.row, nd, o.yb.wide);
-                        zv[i].load(z + (rt + row) * p.z.row, nd, p.z.wide);
-                    }
-                }
-            }
-            if ((st >> t0) & ((2u << S) - 1u))
-                at.template rows<false, true>(t0, nr, st, k0, A2, h, g, ab);
-            else if (plain)
-                at.template rows<true, false>(t0, nr, st, k0, A2, h, g, ab);
+            if ((st >> (b * S)) & ((2u << S) - 1u))
+                at.template rows<true>(b * S, nr, st, k0, A2, h, g, ab);
             else
-                at.template rows<false, false>(t0, nr, st, k0, A2, h, g, ab);
-            __syncwarp();
-            // finish the rows: the sums over states
-#pragma unroll
-            for (int i = 0; i < PERS; ++i) {
-                const int r = nl + LN * i, row = t0 + r;
-                if (nl >= S || row >= nr) break;
-                V gb[TP], qa[TP], hc[TP], s[TP], ys[TP];
-                get<TP>(&sm.gb[r][nl][d0], gb);
-                get<TP>(&sm.qa[r][nl][d0], qa);
-                get<TP>(&sm.hc[r][nl][d0], hc);
-#pragma unroll
-                for (int e = 1; e < LN; ++e) {
-                    V v[TP];
-                    const int from = (nl + e) % LN;
-                    get<TP>(&sm.gb[r][from][d0], v);
-#pragma unroll
-                    for (int q = 0; q < TP; ++q) gb[q] = add2(gb[q], v[q]);
-                    get<TP>(&sm.qa[r][from][d0], v);
-#pragma unroll
-                    for (int q = 0; q < TP; ++q) qa[q] = add2(qa[q], v[q]);
-                    if (z) {
-                        get<TP>(&sm.hc[r][from][d0], v);
-#pragma unroll
-                        for (int q = 0; q < TP; ++q) hc[q] = add2(hc[q], v[q]);
-                    }
-                }
-                get<TP>(&sm.dt[row][d0], s);
-                get<TP>(&sm.yb[row][d0], ys);
-                C xo[TD], so[TD], zo[TD];
-#pragma unroll
-                for (int q = 0; q < TP; ++q) {
-                    const V xe = make2(xv[i].get(2 * q), xv[i].get(2 * q + 1));
-                    const V vx = fma2(gb[q], s[q], mul2(skip[q], ys[q]));
-                    V vs = fma2(qa[q], make2(ln2<C>(), ln2<C>()), mul2(gb[q], xe));
-                    if (p.softplus) vs = mul2(vs, sigmoid2(add2(make2(dv[i].get(2 * q), dv[i].get(2 * q + 1)), bias[q])));
-                    sum_d[q] = fma2(ys[q], xe, sum_d[q]);
-                    sum_bias[q] = add2(sum_bias[q], vs);
-                    xo[2 * q] = vx.x, xo[2 * q + 1] = vx.y;
-                    so[2 * q] = vs.x, so[2 * q + 1] = vs.y;
-                    if (z) {
-                        const V ze = make2(zv[i].get(2 * q), zv[i].get(2 * q + 1)), pe = sigmoid2(ze);
-                        const V vz = mul2(make2(yv[i].get(2 * q), yv[i].get(2 * q + 1)), fma2(skip[q], xe, hc[q]));
-                        zo[2 * q] = vz.x * silu_slope(ze.x, pe.x), zo[2 * q + 1] = vz.y * silu_slope(ze.y, pe.y);
-                    }
-                }
-                Pack<T, TD> out;
-                out.set(xo);
-                out.store(xb + (rt + row) * o.xb.row, nd, o.xb.wide);
-                out.set(so);
-                out.store(dtb + (rt + row) * o.dtb.row, nd, o.dtb.wide);
-                if (z) {
-                    out.set(zo);
-                    out.store(zb + (rt + row) * o.zb.row, nd, o.zb.wide);
-                }
-            }
-            // and the sums over this warp's channels: TD of a row's 2 NP values at a time, from another lane's part on
-            // each, so that the lanes read other banks
-            constexpr int QUADS = LN * (2 * TN / TD);
-            for (int i = lane; i < S * QUADS; i += 32) {
-                const int r = i / QUADS, quad = i % QUADS, m = quad / (2 * TN / TD), half = quad % (2 * TN / TD);
-                C v[TD], e[TD];
-                get<TD>(&sm.part[r][m][half][quad % LD][0], v);
-#pragma unroll
-                for (int f = 1; f < LD; ++f) {
-                    get<TD>(&sm.part[r][m][half][(quad + f) % LD][0], e);
-#pragma unroll
-                    for (int c = 0; c < TD; ++c) v[c] += e[c];
-                }
-#pragma unroll
-                for (int c = 0; c < TD; ++c) {
-                    const int j = half * TD + c;
-                    sm.bc[t0 + r][(j / TN) * NP + m * TN + j % TN] = v[c];
-                }
-            }
-            __syncwarp();
+                at.template rows<false>(b * S, nr, st, k0, A2, h, g, ab);
         }
-        __syncthreads();
+        __syncwarp();
+        // finish the rows
+#pragma unroll 2
+        for (int i = 0; i < PER; ++i) {
+            const int row = nl + LN * i;
+            if (row >= nr) break;
+            Pack<T, 2> xv, dv, yv, zv, out;
+            xv.load(&sm.x[row][c], 2, true);
+            dv.load(&sm.dt_raw[row][c], 2, true);
+            const V gb = *reinterpret_cast<const V *>(&sm.gb[row][c]), qa = *reinterpret_cast<const V *>(&sm.qa[row][c]);
+            const V s = *reinterpret_cast<const V *>(&sm.dt[row][c]), ys = *reinterpret_cast<const V *>(&sm.yb[row][c]);
+            const V xe = make2(xv.get(0), xv.get(1)), sk = make2(skip[0], skip[1]);
+            const V vx = fma2(gb, s, mul2(sk, ys));
+            V vs = fma2(qa, make2(ln2<C>(), ln2<C>()), mul2(gb, xe));
+            if (p.softplus) vs = mul2(vs, sigmoid2(make2(dv.get(0) + bias[0], dv.get(1) + bias[1])));
+            sum_d = fma2(ys, xe, sum_d);
+            if (c < w.nch) sum_bias.x += vs.x;
+            if (c + 1 < w.nch) sum_bias.y += vs.y;
+            const int have = w.nch - c;
+            const int64_t r = rt + row;
+            C q[2] = {vx.x, vx.y};
+            out.set(q);
+            out.store(xb + r * o.xb.row, have, out_wide);
+            q[0] = vs.x, q[1] = vs.y;
+            out.set(q);
+            out.store(dtb + r * o.dtb.row, have, out_wide);
+            if (z) {
+                yv.load(&sm.yb_raw[row][c], 2, true);
+                zv.load(&sm.z[row][c], 2, true);
+                const V hc = *reinterpret_cast<const V *>(&sm.hc[row][c]), ze = make2(zv.get(0), zv.get(1)), pe = sigmoid2(ze);
+                const V inner = mul2(make2(yv.get(0), yv.get(1)), fma2(sk, xe, hc));
+                q[0] = inner.x * silu_slope(ze.x, pe.x), q[1] = inner.y * silu_slope(ze.y, pe.y);
+                out.set(q);
+                out.store(zb + r * o.zb.row, have, out_wide);
+            }
+        }
+        __syncthreads();        // the warps' sums are there, and the staged rows are used up
+        if (rt > w.r0) fetch(rt - R);
         // Bb and Cb: the block's warps, in order, into this block's partial sums [blocks of a group][line, row][group]
         for (int i = threadIdx.x; i < nr * 2 * NP; i += SCAN_WARPS * 32) {
             const int t = i / (2 * NP), j = i % (2 * NP);
             C v = block.warp[0].bc[t][j];
             for (int a = 1; a < live; ++a) v += block.warp[a].bc[t][j];
-            part_bc[(rt + t) * p.groups * 2 * NP + j] = v;
+            part_bc[(int64_t)(rt + t) * p.groups * 2 * NP + j] = v;
         }
     }
     if (w.nch == 0) return;
     const int64_t piece = w.line * p.segs + w.seg;
-    store_part<K>(static_cast<C *>(o.part_a) + piece * dn + part, n, w.nch, lane, ab);
+    at.store(static_cast<C *>(o.part_a) + piece * dn, ab);
     // lanes that finished the same channels
-    C *pd = static_cast<C *>(o.part_d) + piece * p.d + w.c0 + d0, *pb = static_cast<C *>(o.part_bias) + piece * p.d + w.c0 + d0;
 #pragma unroll
-    for (int q = 0; q < TP; ++q) {
-#pragma unroll
-        for (int m = LD; m < 32; m *= 2) {
-            sum_d[q] = add2(sum_d[q], make2(shfl_xor_(sum_d[q].x, m), shfl_xor_(sum_d[q].y, m)));
-            sum_bias[q] = add2(sum_bias[q], make2(shfl_xor_(sum_bias[q].x, m), shfl_xor_(sum_bias[q].y, m)));
-        }
-        if (nl == 0) {
-            if (2 * q < nd) pd[2 * q] = sum_d[q].x, pb[2 * q] = sum_bias[q].x;
-            if (2 * q + 1 < nd) pd[2 * q + 1] = sum_d[q].y, pb[2 * q + 1] = sum_bias[q].y;
-        }
+    for (int m = LD; m < 32; m *= 2) {
+        sum_d = add2(sum_d, make2(shfl_xor_(sum_d.x, m), shfl_xor_(sum_d.y, m)));
+        sum_bias = add2(sum_bias, make2(shfl_xor_(sum_bias.x, m), shfl_xor_(sum_bias.y, m)));
+    }
+    if (nl == 0) {
+        C *pd = static_cast<C *>(o.part_d) + piece * p.d + w.c0 + c, *pb = static_cast<C *>(o.part_bias) + piece * p.d + w.c0 + c;
+        if (c < w.nch) pd[0] = sum_d.x, pb[0] = sum_bias.x;
+        if (c + 1 < w.nch) pd[1] = sum_d.y, pb[1] = sum_bias.y;
     }
 }
 
-// What each segment hands to the row before it, from nothing behind it, and the sum of its steps.
-template <class K> struct ScanEndsSmem {
-    using C = typename K::C;
-    C dt[SCAN_R][K::CW], yb[SCAN_R][K::CW], c[SCAN_R][2 * K::NP];
+// What each segment hands to the row before it, from nothing behind it, and the sum of its steps: a lane per channel, as
+// in the forward.
+template <class T, int NP> struct ScanEndsSmem {
+    using C = typename Elem<T>::C;
+    struct Raw {
+        alignas(16) T dt[SCAN_R][32], yb[SCAN_R][32], z[SCAN_R][32], c[SCAN_R][NP];
+    } raw[2];
+    alignas(16) C dt[SCAN_R][32], yb[SCAN_R][32], c[SCAN_R][NP];
 };
-template <class K, bool POLY, int ROW>
-SELINV_DEVINL void scan_ends_row(const ScanEndsSmem<K> &sm, int t, int d0, int n0, const typename K::V (*A2)[K::TN],
-                                 typename K::V (*g)[K::TN], typename K::V *total)
+template <class T, int NP>
+SELINV_DEVINL void scan_ends_row(const ScanEndsSmem<T, NP> &sm, int t, int lane, const typename Two<typename Elem<T>::C>::V *A2,
+                                 typename Two<typename Elem<T>::C>::V *g)
 {
-    using V = typename K::V;
-    V dt2[K::TP], yb2[K::TP], c2[K::TN];
-    get<K::TP>(&sm.dt[t][d0], dt2);
-    get<K::TP>(&sm.yb[t][d0], yb2);
-    get<K::TN>(&sm.c[t][2 * n0], c2);
-    scan_pairs<K, POLY, ROW>([&](auto poly, int q, int j) {
-        g[q][j] = mul2(decay2<poly.value>(mul2(dt2[q], A2[q][j])), fma2(c2[j], yb2[q], g[q][j]));
-    });
+    using C = typename Elem<T>::C;
+    using V = typename Two<C>::V;
+    const C dt = sm.dt[t][lane], yb = sm.yb[t][lane];
+    const V d2 = make2(dt, dt), y2 = make2(yb, yb);
 #pragma unroll
-    for (int q = 0; q < K::TP; ++q) total[q] = add2(total[q], dt2[q]);
+    for (int j = 0; j < NP / 2; j += 2) {
+        V c[2];
+        get<2>(&sm.c[t][2 * j], c);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) g[j + i] = mul2(exp2_2(mul2(d2, A2[j + i])), fma2(c[i], y2, g[j + i]));
+    }
 }
-template <class K>
+template <class T, int NP>
 __global__ void __launch_bounds__(SCAN_WARPS * 32)
     scan_backward_ends_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ ScanGrads o)
 {
-    using T = typename K::T;
-    using C = typename K::C;
-    using V = typename K::V;
-    constexpr int R = SCAN_R, LN = K::LN, TP = K::TP, TN = K::TN;
+    using C = typename Elem<T>::C;
+    using V = typename Two<C>::V;
+    constexpr int R = SCAN_R;
     extern __shared__ __align__(16) char smem_raw[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    ScanEndsSmem<K> &sm = reinterpret_cast<ScanEndsSmem<K> *>(smem_raw)[warp];
+    ScanEndsSmem<T, NP> &sm = reinterpret_cast<ScanEndsSmem<T, NP> *>(smem_raw)[warp];
     ScanPlace w;
-    if (!scan_place<K>(p, warp, w) || w.r0 >= w.r1 || w.seg == 0) return;
-    const int n = p.n, nl = lane / K::LD, d0 = (lane % K::LD) * K::TD, n0 = nl * TN, nd = w.nch - d0;
-    const T *dt = static_cast<const T *>(p.dt.p) + w.line * p.dt.line + w.c0 + d0;
-    const T *z = p.z.p ? static_cast<const T *>(p.z.p) + w.line * p.z.line + w.c0 + d0 : nullptr;
+    if (!scan_place(p, warp, blockDim.x / 32, 32, w) || w.r0 >= w.r1 || w.seg == 0) return;
+    const int n = p.n;
+    const bool in = lane < w.nch;
+    const T *dt = static_cast<const T *>(p.dt.p) + w.line * p.dt.line + w.c0;
+    const T *z = p.z.p ? static_cast<const T *>(p.z.p) + w.line * p.z.line + w.c0 : nullptr;
     const T *Cc = static_cast<const T *>(p.C.p) + w.line * p.C.line + w.group * p.C_group;
-    const T *yb = static_cast<const T *>(o.yb.p) + w.line * o.yb.line + w.c0 + d0;
-    const int64_t part = (int64_t)w.c0 * n, dn = p.d * n;
-    V A2[TP][TN], g[TP][TN], bias[TP], total[TP];
-    const bool plain = load_decay<K>(p.A, part, n, w.nch, lane, A2) && p.softplus;
-    zero_part<K>(g);
+    const T *yb = static_cast<const T *>(o.yb.p) + w.line * o.yb.line + w.c0;
+    const int64_t own = (int64_t)(w.c0 + lane) * n, dn = p.d * n;
+    V A2[NP / 2], g[NP / 2];
+    load_states<NP>(static_cast<const C *>(p.A) + own, n, in, A2);
 #pragma unroll
-    for (int q = 0; q < TP; ++q) {
-        bias[q] = pair_of<K>(p.dt_bias, w.c0 + d0, nd, q);
-        total[q] = make2((C)0, (C)0);
-    }
-    ScanLoad<K> dl, yl, zl;
-    ScanLoadN<K, 32> cl;
-    auto fetch = [&](int64_t r) {
-        dl.load(dt, p.dt.row, r, w.r1, nd, p.dt.wide, nl);
-        yl.load(yb, o.yb.row, r, w.r1, nd, o.yb.wide, nl);
-        if (z) zl.load(z, p.z.row, r, w.r1, nd, p.z.wide, nl);
-        cl.load(Cc, p.C.row, r, w.r1, n, p.C.wide, lane);
+    for (int j = 0; j < NP / 2; ++j) A2[j] = mul2(A2[j], make2(log2e<C>(), log2e<C>()));
+    zero_states<NP>(g);
+    const C bias = in && p.dt_bias ? static_cast<const C *>(p.dt_bias)[w.c0 + lane] : (C)0;
+    C total = 0;
+    auto fetch = [&](int r, int to) {
+        raw_fetch<32>(sm.raw[to].dt, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
+        raw_fetch<32>(sm.raw[to].yb, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
+        if (z) raw_fetch<32>(sm.raw[to].z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
+        raw_fetch_n<32>(sm.raw[to].c, Cc, p.C.row, r, w.r1, n, p.C.wide, lane);
+        cp_async_commit();
     };
-    int64_t k = p.rows.find(w.r1 - 1);          // the sequence of the row at hand
-    int64_t rt = w.r0 + (w.r1 - w.r0 - 1) / R * R;
-    fetch(rt);
-    for (; rt >= w.r0; rt -= R) {
-        const int nr = (int)min((int64_t)R, w.r1 - rt);
-        int64_t k0 = k;
+    int k = p.rows.find(w.r1 - 1);          // the sequence of the row at hand
+    int rt = w.r0 + (w.r1 - w.r0 - 1) / R * R, now = 0;
+    fetch(rt, 0);
+    for (; rt >= w.r0; rt -= R, now ^= 1) {
+        const int nr = min(R, w.r1 - rt);
+        int k0 = k;
         while (p.rows.start(k0) > rt) --k0;
         const uint32_t st = p.rows.starts(rt, R, k0, lane);
+        const auto &raw = sm.raw[now];
+        cp_async_wait_all();
+        __syncwarp();
+        if (rt > w.r0) fetch(rt - R, now ^ 1);
+        raw_stage_n<32>(sm.c, raw.c, lane);
+        {
+            C a[R], y[R];
 #pragma unroll
-        for (int i = 0; i < K::PER; ++i) {
-            const int row = nl + LN * i;
-            if (row >= R) break;
-            V a[TP], c[TP];
+            for (int t = 0; t < R; ++t) {
+                a[t] = Elem<T>::up(raw.dt[t][lane]) + bias;
+                y[t] = Elem<T>::up(raw.yb[t][lane]);
+            }
+            if (p.softplus) {
 #pragma unroll
-            for (int q = 0; q < TP; ++q) {
-                a[q] = add2(make2(dl.v[i].get(2 * q), dl.v[i].get(2 * q + 1)), bias[q]);
-                if (p.softplus) a[q] = softplus2(a[q]);
-                c[q] = make2(yl.v[i].get(2 * q), yl.v[i].get(2 * q + 1));
-                if (z) {
-                    const V v = make2(zl.v[i].get(2 * q), zl.v[i].get(2 * q + 1));
-                    c[q] = mul2(c[q], mul2(v, sigmoid2(v)));
+                for (int t = 0; t < R; ++t) a[t] = softplus_(a[t]);
+            }
+            if (z) {
+#pragma unroll
+                for (int t = 0; t < R; ++t) {
+                    const C v = Elem<T>::up(raw.z[t][lane]);
+                    y[t] *= v * sigmoid_(v);
                 }
             }
-            put<TP>(&sm.dt[row][d0], a);
-            put<TP>(&sm.yb[row][d0], c);
+#pragma unroll
+            for (int t = 0; t < R; ++t) {
+                sm.dt[t][lane] = a[t];
+                sm.yb[t][lane] = y[t];
+                if (t < nr) total += a[t];
+            }
         }
-        cl.stage(sm.c, lane);
-        if (rt > w.r0) fetch(rt - R);
         __syncwarp();
         for (int t = nr - 1; t >= 0;) {
             if ((st >> (t + 1)) & 1u) {         // the last row of its sequence
                 if (rt + t < p.rows.start(k)) --k;
                 if (o.stateb)
-                    load_part<K>(static_cast<const C *>(o.stateb) + p.rows.number(k, w.line) * dn + part, n, w.nch, lane, g);
+                    load_states<NP>(static_cast<const C *>(o.stateb) + p.rows.number(k, w.line) * dn + own, n, in, g);
                 else
-                    zero_part<K>(g);
+                    zero_states<NP>(g);
             }
             // down to the row behind the next such row
             const uint32_t earlier = st & ((2u << t) - 2u);
             const int te = earlier ? 31 - __clz(earlier) : 0;
-            if (plain) {
-                for (; t - 3 >= te; t -= 4) {
-                    scan_ends_row<K, true, 3>(sm, t, d0, n0, A2, g, total);
-                    scan_ends_row<K, true, 2>(sm, t - 1, d0, n0, A2, g, total);
-                    scan_ends_row<K, true, 1>(sm, t - 2, d0, n0, A2, g, total);
-                    scan_ends_row<K, true, 0>(sm, t - 3, d0, n0, A2, g, total);
-                }
+            for (; t - 3 >= te; t -= 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) scan_ends_row<T, NP>(sm, t - i, lane, A2, g);
             }
-#pragma unroll 1
-            for (; t >= te; --t) scan_ends_row<K, false, 0>(sm, t, d0, n0, A2, g, total);
+            for (; t >= te; --t) scan_ends_row<T, NP>(sm, t, lane, A2, g);
         }
         __syncwarp();
     }
-    scan_leave<K>(p, w, lane, g, total);
+    if (in) {
+        const int64_t piece = w.line * p.segs + w.seg;
+        store_states<NP>(static_cast<C *>(p.ends) + piece * dn + own, n, in, g);
+        static_cast<C *>(p.sums)[piece * p.d + w.c0 + lane] = total;
+    }
 }
 
 // Bb and Cb from the blocks' sums, and Ab, Db, dt_biasb from the segments': the first `bc_blocks` blocks take one
@@ -601,38 +613,30 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Blocks of one group of channels: how many partial sums of B and C there are.
-template <class K> int scan_parts(const ScanArgs &p)
+template <class T, int NP> cudaError_t scan_backward_run(const ScanArgs &p, const ScanGrads &o, cudaStream_t s)
 {
+    using K = ScanBwdTile<T, NP>;
     const int64_t per = p.d / p.groups, tiles = (per + K::CW - 1) / K::CW;
-    return (int)((tiles + SCAN_WARPS - 1) / SCAN_WARPS);
-}
-
-template <class K> cudaError_t scan_backward_run(const ScanArgs &p, const ScanGrads &o, cudaStream_t s)
-{
-    const int parts = scan_parts<K>(p);
+    const int parts = (int)((tiles + SCAN_WARPS - 1) / SCAN_WARPS);
     const dim3 grid((unsigned)(p.lines * p.segs), (unsigned)(p.groups * parts));
-    static_assert(sizeof(ScanBwdSmem<K>) % 16 == 0 && offsetof(ScanBwdSmem<K>, h) % 16 == 0 &&
-                      offsetof(ScanBwdSmem<K>, gb) % 16 == 0 && offsetof(ScanBwdSmem<K>, qa) % 16 == 0 &&
-                      offsetof(ScanBwdSmem<K>, hc) % 16 == 0 && offsetof(ScanBwdSmem<K>, part) % 16 == 0 &&
-                      offsetof(ScanBwdBlock<K>, b) % 16 == 0 && offsetof(ScanBwdBlock<K>, c) % 16 == 0,
-                  "staged rows lie on 16 bytes");
     constexpr int bytes = (int)sizeof(ScanBwdBlock<K>);
     static_assert(bytes <= 227 * 1024, "fits an SM");
     if (p.segs > 1) {
-        constexpr int ends = SCAN_WARPS * (int)sizeof(ScanEndsSmem<K>);
-        static_assert(sizeof(ScanEndsSmem<K>) % 16 == 0 && offsetof(ScanEndsSmem<K>, c) % 16 == 0, "rows on 16 bytes");
+        constexpr int warps = SCAN_WARPS * sizeof(ScanEndsSmem<T, NP>) <= 227 * 1024 ? SCAN_WARPS : SCAN_WARPS / 2;
+        constexpr int ends = warps * (int)sizeof(ScanEndsSmem<T, NP>);
+        const int64_t t32 = (per + 31) / 32;
+        const dim3 g((unsigned)(p.lines * p.segs), (unsigned)(p.groups * ((t32 + warps - 1) / warps)));
         cudaError_t e =
-            cudaFuncSetAttribute(scan_backward_ends_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, ends);
+            cudaFuncSetAttribute(scan_backward_ends_kernel<T, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, ends);
         if (e != cudaSuccess) return e;
-        scan_backward_ends_kernel<K><<<grid, SCAN_WARPS * 32, ends, s>>>(p, o);
+        scan_backward_ends_kernel<T, NP><<<g, warps * 32, ends, s>>>(p, o);
     }
     cudaError_t e = cudaFuncSetAttribute(scan_backward_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     scan_backward_kernel<K><<<grid, SCAN_WARPS * 32, bytes, s>>>(p, o);
-    const int64_t bc = (p.lines * p.rows.rows * p.groups * 2 * K::NP + 255) / 256;
+    const int64_t bc = (p.lines * p.rows.rows * p.groups * 2 * NP + 255) / 256;
     const int64_t params = (p.d * (p.n + 2) + 31) / 32;
-    scan_sums_kernel<typename K::T, K::NP><<<(unsigned)(bc + params), 256, 0, s>>>(p, o, bc, parts);
+    scan_sums_kernel<T, NP><<<(unsigned)(bc + params), 256, 0, s>>>(p, o, bc, parts);
     return cudaGetLastError();
 }
 

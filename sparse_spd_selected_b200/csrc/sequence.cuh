@@ -212,28 +212,8 @@ SELINV_DEVINL float rcp_(float x)
 }
 SELINV_DEVINL double rcp_(double x) { return 1.0 / x; }
 
-// 2^e for a pair whose entries are at most zero, or NaN.  POLY: in the FMA pipe, for a part of the pairs, since the
-// special function unit (16 results a cycle and SM) is what bounds the scan: e = m + f with m the nearest whole
-// number, 2^f by a polynomial of degree 5 on [-1/2, 1/2] (minimax with its first two coefficients held to 1 and ln 2,
-// so that slow decays, e near zero, keep their full accuracy; relative error 1.1e-7, the special function unit's
-// 1.7e-7), m added to its exponent.  Below -126 the result is 2^-126, and so it is for NaN: a step that is NaN
-// reaches the state through its product with x.
-template <bool POLY> SELINV_DEVINL float2 decay2(float2 e)
-{
-    if constexpr (!POLY) return make_float2(exp2_(e.x), exp2_(e.y));
-    e = make_float2(fmaxf(e.x, -126.0f), fmaxf(e.y, -126.0f));
-    const float big = 12582912.0f;      // 1.5 * 2^23: the sum's low bits are the nearest whole number
-    const float2 r = add2(e, make_float2(big, big)), f = add2(e, fma2(r, make_float2(-1.0f, -1.0f), make_float2(big, big)));
-    float2 p = make_float2(0.0013300605351105332f, 0.0013300605351105332f);
-    p = fma2(p, f, make_float2(0.009669691324234009f, 0.009669691324234009f));
-    p = fma2(p, f, make_float2(0.05550558492541313f, 0.05550558492541313f));
-    p = fma2(p, f, make_float2(0.24022282660007477f, 0.24022282660007477f));
-    p = fma2(p, f, make_float2(0.6931471824645996f, 0.6931471824645996f));
-    p = fma2(p, f, make_float2(1.0f, 1.0f));
-    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(r.x) << 23)),
-                       __int_as_float(__float_as_int(p.y) + (__float_as_int(r.y) << 23)));
-}
-template <bool POLY> SELINV_DEVINL double2 decay2(double2 e) { return make_double2(exp2(e.x), exp2(e.y)); }
+SELINV_DEVINL float2 exp2_2(float2 e) { return make_float2(exp2_(e.x), exp2_(e.y)); }
+SELINV_DEVINL double2 exp2_2(double2 e) { return make_double2(exp2(e.x), exp2(e.y)); }
 
 // 1 / (1 + e^-x).
 SELINV_DEVINL float sigmoid_(float x) { return rcp_(1.0f + exp2_(-log2e<float>() * x)); }
@@ -249,27 +229,29 @@ SELINV_DEVINL double2 sigmoid2(double2 x) { return make_double2(sigmoid_(x.x), s
 // d/dx of x sigmoid(x), given p = sigmoid(x).
 template <class C> SELINV_DEVINL C silu_slope(C x, C p) { return p * ((C)1 + x * ((C)1 - p)); }
 
-// log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].  In float log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
-// atanh(s) = s + s q r(q) with q = s^2 and r a minimax cubic on [0, 1/9] (relative error of the sum 4.5e-9): a few
-// rounding steps of relative error also for far negative x, where log(1 + e) itself would lose e's low bits.
+// log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].  In float log1p(e) = e + e^2 r(e), r of degree 7 (minimax
+// for the relative error, 6e-8): a few rounding steps of relative error also for far negative x, where log(1 + e)
+// itself would lose e's low bits, and no second use of the special function unit, which bounds the scan.
 SELINV_DEVINL float max_nan(float a, float b)
 {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-SELINV_DEVINL float2 softplus2(float2 x)
+SELINV_DEVINL float softplus_(float x)
 {
-    const float2 e = make_float2(exp2_(-log2e<float>() * fabsf(x.x)), exp2_(-log2e<float>() * fabsf(x.y)));
-    const float2 w = add2(e, make_float2(2.0f, 2.0f)), s = mul2(e, make_float2(rcp_(w.x), rcp_(w.y))), q = mul2(s, s);
-    float2 r = make_float2(0.1400599330663681f, 0.1400599330663681f);
-    r = fma2(r, q, make_float2(0.14000903069972992f, 0.14000903069972992f));
-    r = fma2(r, q, make_float2(0.2001076340675354f, 0.2001076340675354f));
-    r = fma2(r, q, make_float2(0.3333320915699005f, 0.3333320915699005f));
-    r = fma2(mul2(r, q), s, s);
-    return fma2(r, make_float2(2.0f, 2.0f), make_float2(max_nan(x.x, 0.0f), max_nan(x.y, 0.0f)));
+    const float e = exp2_(-log2e<float>() * fabsf(x));
+    float r = 0.005364798475056887f;
+    r = fmaf(r, e, -0.030065692961215973f);
+    r = fmaf(r, e, 0.07920438051223755f);
+    r = fmaf(r, e, -0.1375378966331482f);
+    r = fmaf(r, e, 0.19153648614883423f);
+    r = fmaf(r, e, -0.24857161939144135f);
+    r = fmaf(r, e, 0.333213210105896f);
+    r = fmaf(r, e, -0.49999648332595825f);
+    return fmaf(e * e, r, e) + max_nan(x, 0.0f);
 }
-SELINV_DEVINL float softplus_(float x) { return softplus2(make_float2(x, x)).x; }
+SELINV_DEVINL float2 softplus2(float2 x) { return make_float2(softplus_(x.x), softplus_(x.y)); }
 SELINV_DEVINL double softplus_(double x) { return x == x ? fmax(x, 0.0) + log1p(exp(-fabs(x))) : x; }
 SELINV_DEVINL double2 softplus2(double2 x) { return make_double2(softplus_(x.x), softplus_(x.y)); }
 
@@ -325,14 +307,14 @@ template <int V, int LO, int HI> SELINV_DEVINL bool scatter_writes(int lane)
 
 struct Rows {
     const int64_t *table;
-    int64_t live, rows;
+    int live, rows;
     // The live sequence that row r lies in (r < rows).
-    SELINV_DEVINL int64_t find(int64_t r) const
+    SELINV_DEVINL int find(int r) const
     {
         if (!table) return 0;
-        int64_t lo = 0, hi = live;
+        int lo = 0, hi = live;
         while (hi - lo > 1) {
-            const int64_t m = (lo + hi) / 2;
+            const int m = (lo + hi) / 2;
             if (table[m] <= r)
                 lo = m;
             else
@@ -340,18 +322,20 @@ struct Rows {
         }
         return lo;
     }
-    SELINV_DEVINL int64_t start(int64_t k) const { return table ? table[k] : 0; }
-    SELINV_DEVINL int64_t end(int64_t k) const { return table ? table[k + 1] : rows; }
-    SELINV_DEVINL int64_t number(int64_t k, int64_t line) const { return table ? table[live + 1 + k] : line; }
-    // Which of the rows r0 .. r0 + n (n <= 31, one more than the n asked for) begin a sequence, given that row r0 lies
-    // in the live sequence k; `rows` itself counts as one.  Every lane of the warp calls it.
-    SELINV_DEVINL uint32_t starts(int64_t r0, int n, int64_t k, int lane) const
+    SELINV_DEVINL int start(int k) const { return table ? (int)table[k] : 0; }
+    SELINV_DEVINL int end(int k) const { return table ? (int)table[k + 1] : rows; }
+    SELINV_DEVINL int64_t number(int k, int64_t line) const { return table ? table[live + 1 + k] : line; }
+    // The sequences without rows, e of them.
+    SELINV_DEVINL int64_t empty(int64_t e) const { return table[2 * (int64_t)live + 1 + e]; }
+    // Which of the rows r0 .. r0 + n (n <= 30) begin a sequence, given that row r0 lies in the live sequence k; `rows`
+    // itself counts as one.  Every lane of the warp calls it.
+    SELINV_DEVINL uint32_t starts(int r0, int n, int k, int lane) const
     {
-        if (!table) return (r0 == 0 ? 1u : 0u) | (r0 + n >= rows ? 1u << (int)(rows - r0) : 0u);
+        if (!table) return (r0 == 0 ? 1u : 0u) | (rows - r0 <= n ? 1u << (rows - r0) : 0u);
         uint32_t bit = 0;
-        if (k + lane <= live) {
-            const int64_t at = table[k + lane] - r0;
-            if (at >= 0 && at <= n) bit = 1u << (int)at;
+        if (lane <= live - k) {
+            const int at = (int)table[k + lane] - r0;
+            if (at >= 0 && at <= n) bit = 1u << at;
         }
         return __reduce_or_sync(FULL_MASK, bit);
     }
@@ -361,7 +345,8 @@ struct Rows {
 // channel of every group lie on 16 bytes, so that packs may be moved whole.
 template <class P> struct Strided {
     P p;
-    int64_t line, row;
+    int64_t line;
+    int row;
     bool wide;
 };
 using In = Strided<const void *>;
@@ -378,8 +363,7 @@ struct ScanArgs {
     Out y;
     void *state_out, *kept;     // may be null
     // lines cut into segments of seg_rows rows: the state each leaves behind from zero, and the sum of its steps
-    int segs;
-    int64_t seg_rows;
+    int segs, seg_rows;
     void *ends, *sums;
 };
 
@@ -422,8 +406,7 @@ struct ConvArgs {
     Out xb;
     void *weightb, *biasb, *stateb_out;
     void *part;
-    int64_t chunk_rows;
-    int chunks;
+    int chunk_rows, chunks;
 };
 
 struct ConvStepArgs {

@@ -5,10 +5,10 @@
 
 namespace selinv {
 
-// The warp tiles of the scan: states padded to NP = 4, 8, 16, 32 or 64; `narrow` 0, 1, 2: four, two or one states
-// per thread, and so as many more warps (float64 has one tile).  The backward takes narrow = 0.
-template <class T> int scan_tile_channels(int n, int narrow);
-template <class T> cudaError_t scan_launch(const ScanArgs &p, int narrow, cudaStream_t s);
+// States are padded to 4, 8, 16, 32 or 64.  Channels of a warp: 32 in the forward.
+constexpr int SCAN_FORWARD_CHANNELS = 32;
+template <class T> int scan_backward_channels(int n);
+template <class T> cudaError_t scan_launch(const ScanArgs &p, cudaStream_t s);
 template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, cudaStream_t s);
 template <class T> cudaError_t scan_step_launch(const ScanStepArgs &p, cudaStream_t s);
 template <class T> cudaError_t conv_launch(const ConvArgs &p, cudaStream_t s);
