@@ -202,8 +202,8 @@ selinv_status conv_check(const selinv_conv_inputs &a)
 // each cost little.
 int64_t conv_chunk(const selinv_conv_inputs &a, bool backward)
 {
-    const int64_t per = 16 / (int64_t)elem(a.dtype), vecs = div_up(a.d, per) * (a.lines > 0 ? a.lines : 1);
-    const int64_t want = (backward ? 512 : 1024) * (int64_t)sm_count(), least = backward ? 32 : 16, most = backward ? 256 : 64;
+    const int64_t per = a.dtype == SELINV_F64 ? 2 : 4, vecs = div_up(a.d, per) * (a.lines > 0 ? a.lines : 1);
+    const int64_t want = 1024 * (int64_t)sm_count(), least = backward ? 32 : 16, most = 128;
     int64_t rows = div_up(a.rows, div_up(want, vecs));
     rows = rows < least ? least : rows > most ? most : rows;
     return div_up(rows, 4) * 4;
@@ -225,7 +225,7 @@ selinv_status conv_args(const selinv_conv_inputs &a, bool backward, ConvArgs &p)
     p.weight = a.weight, p.bias = a.bias, p.state = a.state;
     p.chunk_rows = (int)conv_chunk(a, backward);
     const int64_t chunks = div_up(a.rows, p.chunk_rows);
-    if (div_up(div_up(a.d, 16 / (int64_t)es) * a.lines * chunks, 128) > MAX_GRID_X) return SELINV_ERR_UNSUPPORTED;
+    if (div_up(div_up(a.d, es == 8 ? 2 : 4) * a.lines * chunks, 128) > MAX_GRID_X) return SELINV_ERR_UNSUPPORTED;
     p.chunks = (int)(chunks > 1 ? chunks : 1);
     return SELINV_OK;
 }

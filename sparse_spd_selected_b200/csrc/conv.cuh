@@ -3,10 +3,12 @@
 // with the K - 1 rows before a sequence taken from its state or zero, and its
 // last K - 1 inputs written as its new state.
 //
-// Bounded by memory: x is read and y written once.  A thread keeps 16 bytes
-// of channels (E of them) and runs down a chunk of rows with the last K - 1
-// inputs in registers, so that neighbouring threads read whole lines and each
-// row is fetched once, but for the K - 1 rows before a chunk.
+// Bounded by memory: x is read and y written once.  A thread keeps E
+// neighbouring channels (8 bytes of the 16-bit types, 16 of the others; pairs
+// in one instruction) and runs down a chunk of rows with the last K - 1 inputs
+// in registers, four rows at a time with the next four on their way, so that
+// neighbouring threads read whole lines and each row is fetched once, but for
+// the K - 1 rows before a chunk.
 #pragma once
 
 #include "sequence.cuh"
@@ -15,6 +17,13 @@ namespace selinv {
 namespace {
 
 constexpr int CONV_THREADS = 128;
+constexpr int CONV_U = 4;       // rows at a time
+
+template <class T> struct ConvType {
+    using C = typename Elem<T>::C;
+    using V = typename Two<C>::V;
+    static constexpr int E = sizeof(T) == 8 ? 2 : 4, EP = E / 2;
+};
 
 // A thread's chunk: line, rows [r0, r1), channels [c, c + n).
 struct ConvPlace {
@@ -35,57 +44,100 @@ template <int E> SELINV_DEVINL bool conv_place(const ConvArgs &p, ConvPlace &w)
     return true;
 }
 
-template <class T, int E> SELINV_DEVINL void up_row(const T *p, int n, bool wide, typename Elem<T>::C *v)
+template <class T, int E> SELINV_DEVINL void unpack(const Pack<T, E> &q, typename ConvType<T>::V *v)
 {
-    Pack<T, E> q;
-    q.load(p, n, wide);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = q.get(e);
+    for (int e = 0; e < E / 2; ++e) v[e] = make2(q.get(2 * e), q.get(2 * e + 1));
 }
-template <class T, int E> SELINV_DEVINL void down_row(T *p, int n, bool wide, const typename Elem<T>::C *v)
+template <class T> SELINV_DEVINL void up_row(const T *p, int n, bool wide, typename ConvType<T>::V *v)
 {
+    Pack<T, ConvType<T>::E> q;
+    q.load(p, n, wide);
+    unpack(q, v);
+}
+template <class T> SELINV_DEVINL void down_row(T *p, int n, bool wide, const typename ConvType<T>::V *v)
+{
+    constexpr int E = ConvType<T>::E;
+    typename Elem<T>::C t[E];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) t[2 * e] = v[e].x, t[2 * e + 1] = v[e].y;
     Pack<T, E> q;
-    q.set(v);
+    q.set(t);
     q.store(p, n, wide);
 }
 
+// CONV_U rows of E channels; one branch for all of them.
+template <class T> SELINV_DEVINL void load_rows(const T *p, int stride, bool wide, Pack<T, ConvType<T>::E> *v)
+{
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < CONV_U; ++i) v[i].load(p + (int64_t)i * stride, ConvType<T>::E, true);
+    } else {
+#pragma unroll
+        for (int i = 0; i < CONV_U; ++i) v[i].load(p + (int64_t)i * stride, ConvType<T>::E, false);
+    }
+}
+
 // The K - 1 inputs before row r of the sequence that begins at row `start`.
-template <class T, int K, int E>
+template <class T, int K>
 SELINV_DEVINL void conv_window(const ConvArgs &p, const T *x, int start, int64_t number, int r, int c, int n,
-                               typename Elem<T>::C (*win)[E])
+                               typename ConvType<T>::V (*win)[ConvType<T>::EP])
 {
     const T *state = static_cast<const T *>(p.state);
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
         const int at = r - (K - 1) + i;
         if (at >= start) {
-            up_row<T, E>(x + (int64_t)at * p.x.row, n, p.x.wide, win[i]);
+            up_row(x + (int64_t)at * p.x.row, n, p.x.wide, win[i]);
         } else if (state) {
-            up_row<T, E>(state + (number * (K - 1) + (at - start + K - 1)) * p.d + c, n, false, win[i]);
+            up_row(state + (number * (K - 1) + (at - start + K - 1)) * p.d + c, n, false, win[i]);
         } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) win[i][e] = 0;
+            for (int e = 0; e < ConvType<T>::EP; ++e) win[i][e].x = win[i][e].y = 0;
         }
     }
 }
 
-template <class T, int K, int E>
-SELINV_DEVINL void conv_weights(const ConvArgs &p, const ConvPlace &w, typename Elem<T>::C (*wt)[E],
-                                typename Elem<T>::C *bias)
+template <class T, int K>
+SELINV_DEVINL void conv_weights(const ConvArgs &p, const ConvPlace &w, typename ConvType<T>::V (*wt)[ConvType<T>::EP],
+                                typename ConvType<T>::V *bias)
 {
+    using C = typename Elem<T>::C;
+    constexpr int E = ConvType<T>::E;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-            wt[j][e] = e < w.n ? Elem<T>::up(static_cast<const T *>(p.weight)[(int64_t)(w.c + e) * K + j]) : 0;
-        bias[e] = e < w.n && p.bias ? Elem<T>::up(static_cast<const T *>(p.bias)[w.c + e]) : 0;
+        for (int j = 0; j < K; ++j) {
+            const C v = e < w.n ? Elem<T>::up(static_cast<const T *>(p.weight)[(int64_t)(w.c + e) * K + j]) : (C)0;
+            (e & 1 ? wt[j][e / 2].y : wt[j][e / 2].x) = v;
+        }
+        (e & 1 ? bias[e / 2].y : bias[e / 2].x) =
+            e < w.n && p.bias ? Elem<T>::up(static_cast<const T *>(p.bias)[w.c + e]) : (C)0;
     }
+}
+// sum_j wt_j win_j + bias
+template <int K, int EP, class V> SELINV_DEVINL void conv_taps(const V (*wt)[EP], const V *bias, const V (*win)[EP], V *v)
+{
+#pragma unroll
+    for (int e = 0; e < EP; ++e) {
+        v[e] = bias[e];
+#pragma unroll
+        for (int j = 0; j < K; ++j) v[e] = fma2(wt[j][e], win[j][e], v[e]);
+    }
+}
+template <int K, int M, int EP, class V> SELINV_DEVINL void conv_shift(V (*win)[EP])
+{
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < EP; ++e) win[j][e] = win[j + M][e];
 }
 
 template <class T, int K> __global__ void __launch_bounds__(CONV_THREADS) conv_kernel(const __grid_constant__ ConvArgs p)
 {
     using C = typename Elem<T>::C;
-    constexpr int E = 16 / (int)sizeof(T), U = 4;
+    using V = typename ConvType<T>::V;
+    constexpr int E = ConvType<T>::E, EP = ConvType<T>::EP, U = CONV_U;
     ConvPlace w;
     if (!conv_place<E>(p, w)) return;
     const T *x = static_cast<const T *>(p.x.p) + w.line * p.x.line + w.c;
@@ -101,65 +153,56 @@ template <class T, int K> __global__ void __launch_bounds__(CONV_THREADS) conv_k
         }
     }
     if (w.r0 >= w.r1) return;
-    C wt[K][E], bias[E], win[K - 1 + U][E];
-    conv_weights<T, K, E>(p, w, wt, bias);
+    V wt[K][EP], bias[EP], win[K - 1 + U][EP];
+    conv_weights<T, K>(p, w, wt, bias);
     int k = p.rows.find(w.r0), end = p.rows.end(k);
-    conv_window<T, K, E>(p, x, p.rows.start(k), p.rows.number(k, w.line), w.r0, w.c, w.n, win);
+    conv_window<T, K>(p, x, p.rows.start(k), p.rows.number(k, w.line), w.r0, w.c, w.n, win);
+    const bool whole = w.n == E;
+    Pack<T, E> raw[U];
+    bool ahead = false;         // raw holds the rows r on
     for (int r = w.r0; r < w.r1;) {
-        const int m = min(U, min(w.r1, end) - r);
-        if (m == U) {
-            Pack<T, E> raw[U];
+        const int last = min(w.r1, end);
+        if (whole && r + U <= last) {
+            if (!ahead) load_rows(x + (int64_t)r * p.x.row, p.x.row, p.x.wide, raw);
 #pragma unroll
-            for (int i = 0; i < U; ++i) raw[i].load(x + (int64_t)(r + i) * p.x.row, w.n, p.x.wide);
+            for (int i = 0; i < U; ++i) unpack(raw[i], win[K - 1 + i]);
+            ahead = r + 2 * U <= last;
+            if (ahead) load_rows(x + (int64_t)(r + U) * p.x.row, p.x.row, p.x.wide, raw);
+            V v[U][EP];
 #pragma unroll
-            for (int i = 0; i < U; ++i)
+            for (int i = 0; i < U; ++i) conv_taps<K, EP>(wt, bias, win + i, v[i]);
+            if (p.silu) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) win[K - 1 + i][e] = raw[i].get(e);
+                for (int i = 0; i < U; ++i)
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                C v[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    v[e] = bias[e];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) v[e] += wt[j][e] * win[i + j][e];
-                    if (p.silu) v[e] *= sigmoid_(v[e]);
-                }
-                down_row<T, E>(y + (int64_t)(r + i) * p.y.row, w.n, p.y.wide, v);
+                    for (int e = 0; e < EP; ++e) v[i][e] = mul2(v[i][e], sigmoid2(v[i][e]));
             }
 #pragma unroll
-            for (int i = 0; i < K - 1; ++i)
-#pragma unroll
-                for (int e = 0; e < E; ++e) win[i][e] = win[U + i][e];
+            for (int i = 0; i < U; ++i) down_row(y + (int64_t)(r + i) * p.y.row, E, p.y.wide, v[i]);
+            conv_shift<K, U, EP>(win);
+            r += U;
         } else {
-            for (int i = 0; i < m; ++i) {
-                C v[E];
-                up_row<T, E>(x + (int64_t)(r + i) * p.x.row, w.n, p.x.wide, win[K - 1]);
+            V v[EP];
+            up_row(x + (int64_t)r * p.x.row, w.n, p.x.wide, win[K - 1]);
+            conv_taps<K, EP>(wt, bias, win, v);
+            if (p.silu) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    v[e] = bias[e];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) v[e] += wt[j][e] * win[j][e];
-                    if (p.silu) v[e] *= sigmoid_(v[e]);
-                }
-                down_row<T, E>(y + (int64_t)(r + i) * p.y.row, w.n, p.y.wide, v);
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) win[j][e] = win[j + 1][e];
+                for (int e = 0; e < EP; ++e) v[e] = mul2(v[e], sigmoid2(v[e]));
             }
+            down_row(y + (int64_t)r * p.y.row, w.n, p.y.wide, v);
+            conv_shift<K, 1, EP>(win);
+            ++r;
         }
-        r += m;
         if (r == end) {
             if (state_out) {
                 const int64_t at = p.rows.number(k, w.line) * (K - 1) * p.d + w.c;
 #pragma unroll
-                for (int i = 0; i < K - 1; ++i) down_row<T, E>(state_out + at + i * p.d, w.n, false, win[i]);
+                for (int i = 0; i < K - 1; ++i) down_row(state_out + at + i * p.d, w.n, false, win[i]);
             }
             if (r < w.r1) {
                 ++k;
                 end = p.rows.end(k);
-                conv_window<T, K, E>(p, x, r, p.rows.number(k, w.line), r, w.c, w.n, win);
+                conv_window<T, K>(p, x, r, p.rows.number(k, w.line), r, w.c, w.n, win);
             }
         }
     }
@@ -172,7 +215,8 @@ template <class T, int K>
 __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __grid_constant__ ConvArgs p)
 {
     using C = typename Elem<T>::C;
-    constexpr int E = 16 / (int)sizeof(T);
+    using V = typename ConvType<T>::V;
+    constexpr int E = ConvType<T>::E, EP = ConvType<T>::EP, U = CONV_U;
     ConvPlace w;
     if (!conv_place<E>(p, w)) return;
     const T *x = static_cast<const T *>(p.x.p) + w.line * p.x.line + w.c;
@@ -188,14 +232,17 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
                     stateb_out[at + i * p.d + q] = stateb ? stateb[at + i * p.d + q] : Elem<T>::down((C)0);
         }
     }
-    C wt[K][E], bias[E], wsum[K][E], bsum[E], win[K][E], ring[K][E];
-    conv_weights<T, K, E>(p, w, wt, bias);
+    // win: the inputs from K - 1 rows before row t on; ring: preb likewise
+    V wt[K][EP], bias[EP], wsum[K][EP], bsum[EP], win[K - 1 + U][EP], ring[K - 1 + U][EP];
+    const V none[EP] = {};
+    conv_weights<T, K>(p, w, wt, bias);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        bsum[e] = 0;
+    for (int e = 0; e < EP; ++e) {
+        bsum[e] = none[e];
 #pragma unroll
-        for (int j = 0; j < K; ++j) wsum[j][e] = 0;
+        for (int j = 0; j < K; ++j) wsum[j][e] = none[e];
     }
+    const bool whole = w.n == E;
     if (w.r0 < w.r1) {
         int k = p.rows.find(w.r0);
         for (int r = w.r0; r < w.r1; ++k) {
@@ -203,63 +250,111 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
             const int64_t number = p.rows.number(k, w.line);
             const bool head = start >= w.r0;                       // this chunk holds the sequence's first row
             const int m0 = head ? start - (K - 1) : w.r0, m1 = min(end, w.r1);
-            conv_window<T, K, E>(p, x, start, number, r, w.c, w.n, win);
+            conv_window<T, K>(p, x, start, number, r, w.c, w.n, win);
 #pragma unroll
-            for (int j = 0; j < K; ++j)
+            for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-                for (int e = 0; e < E; ++e) ring[j][e] = 0;
-            for (int t = r; t - (K - 1) < m1; ++t) {
+                for (int e = 0; e < EP; ++e) ring[j][e] = none[e];
+            Pack<T, E> xr[U], yr[U];
+            bool ahead = false;
+            for (int t = r; t - (K - 1) < m1;) {
+                // U rows t .. t + U - 1 of this chunk whose outputs are rows of this sequence that no final state holds
+                const auto plain = [&](int s) {
+                    return whole && s + U <= min(end, w.r1) && s - (K - 1) >= max(start, w.r0) && (!stateb || s + U - K < end - (K - 1));
+                };
+                if (plain(t)) {
+                    if (!ahead) {
+                        load_rows(x + (int64_t)t * p.x.row, p.x.row, p.x.wide, xr);
+                        load_rows(yb + (int64_t)t * p.yb.row, p.yb.row, p.yb.wide, yr);
+                    }
+                    V g[U][EP];
 #pragma unroll
-                for (int j = 0; j < K - 1; ++j)
+                    for (int i = 0; i < U; ++i) {
+                        unpack(xr[i], win[K - 1 + i]);
+                        unpack(yr[i], g[i]);
+                    }
+                    ahead = plain(t + U);
+                    if (ahead) {
+                        load_rows(x + (int64_t)(t + U) * p.x.row, p.x.row, p.x.wide, xr);
+                        load_rows(yb + (int64_t)(t + U) * p.yb.row, p.yb.row, p.yb.wide, yr);
+                    }
+                    if (p.silu) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) ring[j][e] = ring[j + 1][e];
-                if (t < end) {
-                    C g[E];
-                    up_row<T, E>(x + (int64_t)t * p.x.row, w.n, p.x.wide, win[K - 1]);
-                    up_row<T, E>(yb + (int64_t)t * p.yb.row, w.n, p.yb.wide, g);
+                        for (int i = 0; i < U; ++i) {
+                            V v[EP];
+                            conv_taps<K, EP>(wt, bias, win + i, v);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        if (p.silu) {
-                            C v = bias[e];
-#pragma unroll
-                            for (int j = 0; j < K; ++j) v += wt[j][e] * win[j][e];
-                            g[e] *= silu_slope(v, sigmoid_(v));
-                        }
-                        ring[K - 1][e] = g[e];
-                        if (t < w.r1) {
-                            bsum[e] += g[e];
-#pragma unroll
-                            for (int j = 0; j < K; ++j) wsum[j][e] += g[e] * win[j][e];
+                            for (int e = 0; e < EP; ++e) g[i][e] = mul2(g[i][e], silu_slope2(v[e], sigmoid2(v[e])));
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < K - 1; ++j)
+                    for (int i = 0; i < U; ++i) {
+                        V v[EP];
 #pragma unroll
-                        for (int e = 0; e < E; ++e) win[j][e] = win[j + 1][e];
+                        for (int e = 0; e < EP; ++e) {
+                            ring[K - 1 + i][e] = g[i][e];
+                            bsum[e] = add2(bsum[e], g[i][e]);
+                            v[e] = mul2(wt[K - 1][e], ring[i][e]);
+#pragma unroll
+                            for (int j = 0; j < K; ++j) {
+                                wsum[j][e] = fma2(g[i][e], win[i + j][e], wsum[j][e]);
+                                if (j) v[e] = fma2(wt[K - 1 - j][e], ring[i + j][e], v[e]);
+                            }
+                        }
+                        down_row(xb + (int64_t)(t + i - (K - 1)) * p.xb.row, E, p.xb.wide, v);
+                    }
+                    conv_shift<K, U, EP>(win);
+                    conv_shift<K, U, EP>(ring);
+                    t += U;
+                    continue;
+                }
+                if (t < end) {
+                    V g[EP];
+                    up_row(x + (int64_t)t * p.x.row, w.n, p.x.wide, win[K - 1]);
+                    up_row(yb + (int64_t)t * p.yb.row, w.n, p.yb.wide, g);
+                    if (p.silu) {
+                        V v[EP];
+                        conv_taps<K, EP>(wt, bias, win, v);
+#pragma unroll
+                        for (int e = 0; e < EP; ++e) g[e] = mul2(g[e], silu_slope2(v[e], sigmoid2(v[e])));
+                    }
+#pragma unroll
+                    for (int e = 0; e < EP; ++e) {
+                        ring[K - 1][e] = g[e];
+                        if (t < w.r1) {
+                            bsum[e] = add2(bsum[e], g[e]);
+#pragma unroll
+                            for (int j = 0; j < K; ++j) wsum[j][e] = fma2(g[e], win[j][e], wsum[j][e]);
+                        }
+                    }
+                    conv_shift<K, 1, EP>(win);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) ring[K - 1][e] = 0;
+                    for (int e = 0; e < EP; ++e) ring[K - 1][e] = none[e];
                 }
                 const int m = t - (K - 1);
-                if (m < m0) continue;
-                C v[E];
+                if (m >= m0) {
+                    V v[EP];
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    v[e] = 0;
+                    for (int e = 0; e < EP; ++e) {
+                        v[e] = mul2(wt[K - 1][e], ring[0][e]);
 #pragma unroll
-                    for (int j = 0; j < K; ++j) v[e] += wt[j][e] * ring[K - 1 - j][e];
+                        for (int j = 1; j < K; ++j) v[e] = fma2(wt[K - 1 - j][e], ring[j][e], v[e]);
+                    }
+                    const int j = m - (end - (K - 1));             // the row of the final state that is this input
+                    if (stateb && j >= 0) {
+                        V s[EP];
+                        up_row(stateb + (number * (K - 1) + j) * p.d + w.c, w.n, false, s);
+#pragma unroll
+                        for (int e = 0; e < EP; ++e) v[e] = add2(v[e], s[e]);
+                    }
+                    if (m >= start)
+                        down_row(xb + (int64_t)m * p.xb.row, w.n, p.xb.wide, v);
+                    else if (stateb_out)
+                        down_row(stateb_out + (number * (K - 1) + (m - start + K - 1)) * p.d + w.c, w.n, false, v);
                 }
-                const int j = m - (end - (K - 1));             // the row of the final state that is this input
-                if (stateb && j >= 0) {
-                    C s[E];
-                    up_row<T, E>(stateb + (number * (K - 1) + j) * p.d + w.c, w.n, false, s);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[e] += s[e];
-                }
-                if (m >= start)
-                    down_row<T, E>(xb + (int64_t)m * p.xb.row, w.n, p.xb.wide, v);
-                else if (stateb_out)
-                    down_row<T, E>(stateb_out + (number * (K - 1) + (m - start + K - 1)) * p.d + w.c, w.n, false, v);
+                conv_shift<K, 1, EP>(ring);
+                ++t;
             }
             r = m1;
         }
@@ -269,8 +364,8 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
     for (int e = 0; e < E; ++e)
         if (e < w.n) {
 #pragma unroll
-            for (int j = 0; j < K; ++j) part[j * p.d + e] = wsum[j][e];
-            part[K * p.d + e] = bsum[e];
+            for (int j = 0; j < K; ++j) part[j * p.d + e] = e & 1 ? wsum[j][e / 2].y : wsum[j][e / 2].x;
+            part[K * p.d + e] = e & 1 ? bsum[e / 2].y : bsum[e / 2].x;
         }
 }
 
@@ -343,14 +438,14 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_step_kernel(const __grid_co
 
 template <class T, int K> cudaError_t conv_run(const ConvArgs &p, cudaStream_t s)
 {
-    constexpr int E = 16 / (int)sizeof(T);
+    constexpr int E = ConvType<T>::E;
     const int64_t threads = (p.d + E - 1) / E * p.lines * p.chunks;
     conv_kernel<T, K><<<(unsigned)((threads + CONV_THREADS - 1) / CONV_THREADS), CONV_THREADS, 0, s>>>(p);
     return cudaGetLastError();
 }
 template <class T, int K> cudaError_t conv_backward_run(const ConvArgs &p, cudaStream_t s)
 {
-    constexpr int E = 16 / (int)sizeof(T);
+    constexpr int E = ConvType<T>::E;
     const int64_t threads = (p.d + E - 1) / E * p.lines * p.chunks;
     conv_backward_kernel<T, K><<<(unsigned)((threads + CONV_THREADS - 1) / CONV_THREADS), CONV_THREADS, 0, s>>>(p);
     const dim3 grid((unsigned)((p.d + 31) / 32), (unsigned)(K + 1));

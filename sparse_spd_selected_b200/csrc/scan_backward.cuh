@@ -213,12 +213,16 @@ template <class K> struct ScanBwd {
         for (int i = lane; i < SCAN_P * PAIRS; i += 32) {
             const int r = i / PAIRS, pair = i % PAIRS, half = pair % HALVES, chunk = pair / HALVES;
             const int m = chunk / K::CHUNKS, ch = chunk % K::CHUNKS;
-            V v = *reinterpret_cast<const V *>(&sm.part[r][m][ch][chunk % K::LD][2 * half]);
+            V v[K::LD];
 #pragma unroll
-            for (int f = 1; f < K::LD; ++f)
-                v = add2(v, *reinterpret_cast<const V *>(&sm.part[r][m][ch][(chunk + f) % K::LD][2 * half]));
+            for (int f = 0; f < K::LD; ++f)
+                v[f] = *reinterpret_cast<const V *>(&sm.part[r][m][ch][(chunk + f) % K::LD][2 * half]);
+#pragma unroll
+            for (int s = K::LD / 2; s > 0; s /= 2)
+#pragma unroll
+                for (int f = 0; f < s; ++f) v[f] = add2(v[f], v[f + s]);
             const int j = ch * K::Q + 2 * half;         // among B's states and then C's of lane group m
-            *reinterpret_cast<V *>(&sm.bc[t + r][(j / SN) * K::NP + m * SN + j % SN]) = v;
+            *reinterpret_cast<V *>(&sm.bc[t + r][(j / SN) * K::NP + m * SN + j % SN]) = v[0];
         }
     }
 };
@@ -289,6 +293,19 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
     C *part_bc = static_cast<C *>(o.part_bc) +
                  (((int64_t)bi * p.lines + w.line) * p.rows.rows * p.groups + w.group) * 2 * NP;
     const bool out_wide = o.xb.wide && o.dtb.wide && (!z || o.zb.wide);
+    // rows rt + r, rt + r + LN, ... of an output, below rt + rows
+    const auto put_rows = [](T *to, int stride, int rt, int r, int rows, int have, bool wide, const auto &v) {
+        constexpr int F = sizeof(v) / sizeof(V);
+        to += (int64_t)(rt + r) * stride;
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            if (r + LN * i >= rows) break;
+            const C q[2] = {v[i].x, v[i].y};
+            Pack<T, 2> out;
+            out.set(q);
+            out.store(to + (int64_t)(LN * i) * stride, have, wide);
+        }
+    };
 
     auto fetch = [&](int r) {
         raw_fetch<CW>(sm.x, x, p.x.row, r, w.r1, w.nch, p.x.wide, lane);
@@ -380,39 +397,58 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
                 at.template rows<false>(b * S, nr, st, k0, A2, h, g, ab);
         }
         __syncwarp();
-        // finish the rows
-#pragma unroll 2
-        for (int i = 0; i < PER; ++i) {
-            const int row = nl + LN * i;
-            if (row >= nr) break;
-            Pack<T, 2> xv, dv, yv, zv, out;
-            xv.load(&sm.x[row][c], 2, true);
-            dv.load(&sm.dt_raw[row][c], 2, true);
-            const V gb = *reinterpret_cast<const V *>(&sm.gb[row][c]), qa = *reinterpret_cast<const V *>(&sm.qa[row][c]);
-            const V s = *reinterpret_cast<const V *>(&sm.dt[row][c]), ys = *reinterpret_cast<const V *>(&sm.yb[row][c]);
-            const V xe = make2(xv.get(0), xv.get(1)), sk = make2(skip[0], skip[1]);
-            const V vx = fma2(gb, s, mul2(sk, ys));
-            V vs = fma2(qa, make2(ln2<C>(), ln2<C>()), mul2(gb, xe));
-            if (p.softplus) vs = mul2(vs, sigmoid2(make2(dv.get(0) + bias[0], dv.get(1) + bias[1])));
-            sum_d = fma2(ys, xe, sum_d);
-            if (c < w.nch) sum_bias.x += vs.x;
-            if (c + 1 < w.nch) sum_bias.y += vs.y;
-            const int have = w.nch - c;
-            const int64_t r = rt + row;
-            C q[2] = {vx.x, vx.y};
-            out.set(q);
-            out.store(xb + r * o.xb.row, have, out_wide);
-            q[0] = vs.x, q[1] = vs.y;
-            out.set(q);
-            out.store(dtb + r * o.dtb.row, have, out_wide);
+        // finish the rows, four of a lane's at a time: all loads, then the arithmetic, then the stores
+        constexpr int F = PER < 4 ? PER : 4;
+#pragma unroll
+        for (int i0 = 0; i0 < PER; i0 += F) {
+            V xe[F], de[F], gb[F], qa[F], s[F], ys[F], vx[F], vs[F];
+            const V sk = make2(skip[0], skip[1]);
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                const int row = min(nl + LN * (i0 + i), R - 1);
+                Pack<T, 2> v;
+                v.load(&sm.x[row][c], 2, true);
+                xe[i] = make2(v.get(0), v.get(1));
+                v.load(&sm.dt_raw[row][c], 2, true);
+                de[i] = make2(v.get(0) + bias[0], v.get(1) + bias[1]);
+                gb[i] = *reinterpret_cast<const V *>(&sm.gb[row][c]);
+                qa[i] = *reinterpret_cast<const V *>(&sm.qa[row][c]);
+                s[i] = *reinterpret_cast<const V *>(&sm.dt[row][c]);
+                ys[i] = *reinterpret_cast<const V *>(&sm.yb[row][c]);
+            }
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                vx[i] = fma2(gb[i], s[i], mul2(sk, ys[i]));
+                vs[i] = fma2(qa[i], make2(ln2<C>(), ln2<C>()), mul2(gb[i], xe[i]));
+            }
+            if (p.softplus) {
+#pragma unroll
+                for (int i = 0; i < F; ++i) vs[i] = mul2(vs[i], sigmoid2(de[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                const bool have = nl + LN * (i0 + i) < nr;
+                if (have) sum_d = fma2(ys[i], xe[i], sum_d);
+                if (have && c < w.nch) sum_bias.x += vs[i].x;
+                if (have && c + 1 < w.nch) sum_bias.y += vs[i].y;
+            }
+            put_rows(xb, o.xb.row, rt, nl + LN * i0, nr, w.nch - c, out_wide, vx);
+            put_rows(dtb, o.dtb.row, rt, nl + LN * i0, nr, w.nch - c, out_wide, vs);
             if (z) {
-                yv.load(&sm.yb_raw[row][c], 2, true);
-                zv.load(&sm.z[row][c], 2, true);
-                const V hc = *reinterpret_cast<const V *>(&sm.hc[row][c]), ze = make2(zv.get(0), zv.get(1)), pe = sigmoid2(ze);
-                const V inner = mul2(make2(yv.get(0), yv.get(1)), fma2(sk, xe, hc));
-                q[0] = inner.x * silu_slope(ze.x, pe.x), q[1] = inner.y * silu_slope(ze.y, pe.y);
-                out.set(q);
-                out.store(zb + r * o.zb.row, have, out_wide);
+#pragma unroll
+                for (int i = 0; i < F; ++i) {
+                    const int row = min(nl + LN * (i0 + i), R - 1);
+                    Pack<T, 2> v;
+                    v.load(&sm.yb_raw[row][c], 2, true);
+                    ys[i] = make2(v.get(0), v.get(1));
+                    v.load(&sm.z[row][c], 2, true);
+                    de[i] = make2(v.get(0), v.get(1));
+                    s[i] = *reinterpret_cast<const V *>(&sm.hc[row][c]);
+                }
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+                    vs[i] = mul2(mul2(ys[i], fma2(sk, xe[i], s[i])), silu_slope2(de[i], sigmoid2(de[i])));
+                put_rows(zb, o.zb.row, rt, nl + LN * i0, nr, w.nch - c, out_wide, vs);
             }
         }
         __syncthreads();        // the warps' sums are there, and the staged rows are used up

@@ -229,6 +229,13 @@ SELINV_DEVINL double2 sigmoid2(double2 x) { return make_double2(sigmoid_(x.x), s
 // d/dx of x sigmoid(x), given p = sigmoid(x).
 template <class C> SELINV_DEVINL C silu_slope(C x, C p) { return p * ((C)1 + x * ((C)1 - p)); }
 
+SELINV_DEVINL float2 silu_slope2(float2 x, float2 p)
+{
+    const float2 one = make_float2(1.0f, 1.0f);
+    return mul2(p, fma2(x, fma2(p, make_float2(-1.0f, -1.0f), one), one));
+}
+SELINV_DEVINL double2 silu_slope2(double2 x, double2 p) { return make_double2(silu_slope(x.x, p.x), silu_slope(x.y, p.y)); }
+
 // log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].  In float log1p(e) = e + e^2 r(e), r of degree 7 (minimax
 // for the relative error, 6e-8): a few rounding steps of relative error also for far negative x, where log(1 + e)
 // itself would lose e's low bits, and no second use of the special function unit, which bounds the scan.
