@@ -90,26 +90,23 @@ selinv_status scan_check(const selinv_scan_inputs &a)
     return SELINV_OK;
 }
 
-// Channels of a warp.
-int64_t warp_channels(const selinv_scan_inputs &a, bool backward)
-{
-    if (!backward) return SCAN_FORWARD_CHANNELS;
-    return with_type(a.dtype, [&](auto t) { return scan_backward_channels<decltype(t)>((int)a.n); });
-}
-
 // How a scan is spread over the GPU.
 struct Spread {
-    int segs;
+    int lanes, segs;                        // lanes of a channel (forward), segments of a line
     int64_t seg_rows, tiles, blocks;        // tiles of a warp's channels and blocks of tiles, over all groups
 };
 Spread scan_spread(const selinv_scan_inputs &a, bool backward)
 {
-    const int64_t tiles = div_up(a.d / a.groups, warp_channels(a, backward));
-    Spread s{1, a.rows, a.groups * tiles, a.groups * div_up(tiles, SCAN_BLOCK_TILES)};
+    const int n = (int)a.n;
+    const int64_t per = a.d / a.groups, sms = sm_count(), lines = a.lines > 0 ? a.lines : 1;
+    const auto blocks = [&](int64_t channels) { return lines * a.groups * div_up(div_up(per, channels), SCAN_BLOCK_TILES); };
+    Spread s{scan_least_lanes(n), 1, a.rows, 0, 0};
+    int64_t cw = backward ? with_type(a.dtype, [&](auto t) { return scan_backward_channels<decltype(t)>(n); }) : 32 / s.lanes;
+    s.tiles = a.groups * div_up(per, cw);
+    s.blocks = a.groups * div_up(div_up(per, cw), SCAN_BLOCK_TILES);
     // Lines are cut where their blocks do not fill the GPU: into so many segments that all are resident at once (four
     // blocks per SM forward, two backward), none under 64 rows.
-    const int64_t room = (backward ? 2 : 4) * (int64_t)sm_count() / (a.lines * s.blocks > 0 ? a.lines * s.blocks : 1);
-    const int64_t most = a.rows / 64 > 1 ? a.rows / 64 : 1;
+    const int64_t room = (backward ? 2 : 4) * sms / (lines * s.blocks), most = a.rows / 64 > 1 ? a.rows / 64 : 1;
     s.segs = (int)(room < 2 ? 1 : room < most ? room : most);
     s.seg_rows = div_up(div_up(a.rows, s.segs), SCAN_KEEP_ROWS) * SCAN_KEEP_ROWS;
     if (s.seg_rows < SCAN_KEEP_ROWS) s.seg_rows = SCAN_KEEP_ROWS;
@@ -262,7 +259,7 @@ selinv_status selinv_selective_scan(const selinv_scan_inputs *a, const selinv_vi
     p.y = out_of(*y, es, a->groups > 1 ? a->d / a->groups : 0);
     p.state_out = state_out, p.kept = kept;
     p.ends = static_cast<char *>(workspace) + w.ends, p.sums = static_cast<char *>(workspace) + w.sums;
-    return from_cuda(with_type(a->dtype, [&](auto t) { return scan_launch<decltype(t)>(p, s); }));
+    return from_cuda(with_type(a->dtype, [&](auto t) { return scan_launch<decltype(t)>(p, spread.lanes, s); }));
 }
 
 selinv_status selinv_selective_scan_backward(const selinv_scan_inputs *a, const selinv_scan_grads *g, void *workspace,

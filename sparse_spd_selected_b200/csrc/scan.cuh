@@ -88,24 +88,32 @@ template <int N> SELINV_DEVINL void put(double *p, const double2 *v)
     for (int i = 0; i < N; ++i) *reinterpret_cast<double2 *>(p + 2 * i) = v[i];
 }
 
-// Starts copying CW channels (nch of them exist) of rows r .. r1 - 1, at most SCAN_R, into `to`.
-template <int CW, class T>
+// Starts copying CW channels (nch of them exist) of rows r .. r1 - 1, at most SCAN_R, into `to`.  FULL: all channels, all
+// rows, on 16 bytes; straight code, since a few warps wait for nothing but their own instructions here.
+template <int CW, bool FULL, class T>
 SELINV_DEVINL void raw_fetch(T (*to)[CW], const T *from, int stride, int r, int r1, int nch, bool wide, int lane)
 {
     constexpr int E = 16 / (int)sizeof(T), LANES = CW / E, ROWS = 32 / LANES;
     static_assert(CW % E == 0 && LANES <= 32, "a warp copies whole rows");
+    const int row = lane / LANES, e = (lane % LANES) * E;
+    if (FULL) {
+        const T *at = from + ((int64_t)(r + row) * stride + e);
+        if (ROWS <= SCAN_R || row < SCAN_R) {
+#pragma unroll
+            for (int i = 0; i < SCAN_R; i += ROWS) cp_async16(&to[row + i][e], at + (int64_t)i * stride);
+        }
+        return;
+    }
     const int nr = min(SCAN_R, r1 - r);
-    from += (int64_t)r * stride;
     if (wide && nch == CW) {
-        const int row = lane / LANES, e = (lane % LANES) * E;
-        const T *at = from + (int64_t)row * stride + e;
+        const T *at = from + ((int64_t)(r + row) * stride + e);
 #pragma unroll
         for (int i = 0; i < SCAN_R; i += ROWS)
             if (row + i < nr) cp_async16(&to[row + i][e], at + (int64_t)i * stride);
     } else {
         for (int c = lane; c < nch; c += 32) {
 #pragma unroll 4
-            for (int i = 0; i < nr; ++i) to[i][c] = from[(int64_t)i * stride + c];
+            for (int i = 0; i < nr; ++i) to[i][c] = from[(int64_t)(r + i) * stride + c];
         }
     }
 }
@@ -117,17 +125,16 @@ SELINV_DEVINL void raw_prefetch(const T *from, int stride, int r, int r1, int nc
 }
 // The same of B or C [rows, n] into rows of NP, dealt out over THREADS threads; with zeros where states or rows are not
 // there (they take part in sums over channels).
-template <int THREADS, class T, int NP>
+template <int THREADS, bool FULL, class T, int NP>
 SELINV_DEVINL void raw_fetch_n(T (*to)[NP], const T *from, int stride, int r, int r1, int n, bool wide, int thread)
 {
     constexpr int E = sizeof(T) == 2 ? 4 : 16 / (int)sizeof(T), ROW = NP / E;      // 8 or 16 bytes at a time
     const int nr = min(SCAN_R, r1 - r);
-    from += (int64_t)r * stride;
 #pragma unroll
     for (int i = thread; i < SCAN_R * ROW; i += THREADS) {
         const int row = i / ROW, e = (i % ROW) * E;
-        const T *at = from + (int64_t)row * stride + e;
-        if (wide && row < nr && e + E <= n) {
+        const T *at = from + ((int64_t)(r + row) * stride + e);
+        if (FULL || (wide && row < nr && e + E <= n)) {
             if constexpr (sizeof(T) == 2)
                 cp_async8(&to[row][e], at);
             else

@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
     const int tiles = (p.rows.rows + R - 1) / R;
     const int per = (int)(p.d / p.groups), tiles_c = (per + CW - 1) / CW;
     const int blocks = (tiles_c + SCAN_WARPS - 1) / SCAN_WARPS, bi = (int)blockIdx.y % blocks;
-    const int live = min(SCAN_WARPS, tiles_c - bi * SCAN_WARPS);
     C *part_bc = static_cast<C *>(o.part_bc) +
                  (((int64_t)bi * p.lines + w.line) * p.rows.rows * p.groups + w.group) * 2 * NP;
     const bool out_wide = o.xb.wide && o.dtb.wide && (!z || o.zb.wide);
@@ -297,24 +296,37 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
     const auto put_rows = [](T *to, int stride, int rt, int r, int rows, int have, bool wide, const auto &v) {
         constexpr int F = sizeof(v) / sizeof(V);
         to += (int64_t)(rt + r) * stride;
+        Pack<T, 2> out[F];
 #pragma unroll
         for (int i = 0; i < F; ++i) {
-            if (r + LN * i >= rows) break;
             const C q[2] = {v[i].x, v[i].y};
-            Pack<T, 2> out;
-            out.set(q);
-            out.store(to + (int64_t)(LN * i) * stride, have, wide);
+            out[i].set(q);
+        }
+        if (wide && have >= 2 && r + LN * (F - 1) < rows) {
+#pragma unroll
+            for (int i = 0; i < F; ++i) out[i].store(to + (int64_t)(LN * i) * stride, 2, true);
+        } else {
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+                if (r + LN * i < rows) out[i].store(to + (int64_t)(LN * i) * stride, have, false);
         }
     };
-
-    auto fetch = [&](int r) {
-        raw_fetch<CW>(sm.x, x, p.x.row, r, w.r1, w.nch, p.x.wide, lane);
-        raw_fetch<CW>(sm.dt_raw, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
-        raw_fetch<CW>(sm.yb_raw, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
-        if (z) raw_fetch<CW>(sm.z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
-        raw_fetch_n<SCAN_WARPS * 32>(block.b_raw, B, p.B.row, r, w.r1, n, p.B.wide, threadIdx.x);
-        raw_fetch_n<SCAN_WARPS * 32>(block.c_raw, Cc, p.C.row, r, w.r1, n, p.C.wide, threadIdx.x);
+    const bool full = p.x.wide && p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.B.wide && p.C.wide && w.nch == CW && n == NP;
+    auto fetch_as = [&](auto whole, int r) {
+        constexpr bool F = whole.value;
+        raw_fetch<CW, F>(sm.x, x, p.x.row, r, w.r1, w.nch, p.x.wide, lane);
+        raw_fetch<CW, F>(sm.dt_raw, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
+        raw_fetch<CW, F>(sm.yb_raw, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
+        if (z) raw_fetch<CW, F>(sm.z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
+        raw_fetch_n<SCAN_WARPS * 32, F>(block.b_raw, B, p.B.row, r, w.r1, n, p.B.wide, threadIdx.x);
+        raw_fetch_n<SCAN_WARPS * 32, F>(block.c_raw, Cc, p.C.row, r, w.r1, n, p.C.wide, threadIdx.x);
         cp_async_commit();
+    };
+    auto fetch = [&](int r) {
+        if (full && r + R <= w.r1)
+            fetch_as(std::true_type(), r);
+        else
+            fetch_as(std::false_type(), r);
     };
     int rt = w.r0 + (w.r1 > w.r0 ? (w.r1 - w.r0 - 1) / R * R : 0);
     if (w.r1 > w.r0) fetch(rt);
@@ -454,11 +466,13 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
         __syncthreads();        // the warps' sums are there, and the staged rows are used up
         if (rt > w.r0) fetch(rt - R);
         // Bb and Cb: the block's warps, in order, into this block's partial sums [blocks of a group][line, row][group]
-        for (int i = threadIdx.x; i < nr * 2 * NP; i += SCAN_WARPS * 32) {
+#pragma unroll
+        for (int i = threadIdx.x; i < R * 2 * NP; i += SCAN_WARPS * 32) {
             const int t = i / (2 * NP), j = i % (2 * NP);
-            C v = block.warp[0].bc[t][j];
-            for (int a = 1; a < live; ++a) v += block.warp[a].bc[t][j];
-            part_bc[(int64_t)(rt + t) * p.groups * 2 * NP + j] = v;
+            C v = 0;
+#pragma unroll
+            for (int a = 0; a < SCAN_WARPS; ++a) v += block.warp[a].bc[t][j];       // zero where a warp has no channels
+            if (t < nr) part_bc[(int64_t)(rt + t) * p.groups * 2 * NP + j] = v;
         }
     }
     if (w.nch == 0) return;
@@ -528,12 +542,20 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
     zero_states<NP>(g);
     const C bias = in && p.dt_bias ? static_cast<const C *>(p.dt_bias)[w.c0 + lane] : (C)0;
     C total = 0;
-    auto fetch = [&](int r, int to) {
-        raw_fetch<32>(sm.raw[to].dt, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
-        raw_fetch<32>(sm.raw[to].yb, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
-        if (z) raw_fetch<32>(sm.raw[to].z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
-        raw_fetch_n<32>(sm.raw[to].c, Cc, p.C.row, r, w.r1, n, p.C.wide, lane);
+    const bool full = p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.C.wide && w.nch == 32 && n == NP;
+    auto fetch_as = [&](auto whole, int r, int to) {
+        constexpr bool F = whole.value;
+        raw_fetch<32, F>(sm.raw[to].dt, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
+        raw_fetch<32, F>(sm.raw[to].yb, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
+        if (z) raw_fetch<32, F>(sm.raw[to].z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
+        raw_fetch_n<32, F>(sm.raw[to].c, Cc, p.C.row, r, w.r1, n, p.C.wide, lane);
         cp_async_commit();
+    };
+    auto fetch = [&](int r, int to) {
+        if (full && r + R <= w.r1)
+            fetch_as(std::true_type(), r, to);
+        else
+            fetch_as(std::false_type(), r, to);
     };
     int k = p.rows.find(w.r1 - 1);          // the sequence of the row at hand
     int rt = w.r0 + (w.r1 - w.r0 - 1) / R * R, now = 0;
@@ -616,6 +638,7 @@ __global__ void __launch_bounds__(256)
         const int64_t at = i / (2 * NP), r = at / p.groups, g = at % p.groups;
         if (m >= p.n) return;
         C v = 0;
+#pragma unroll 8
         for (int b = 0; b < parts; ++b) v += static_cast<const C *>(o.part_bc)[b * total + i];
         const int64_t line = r / p.rows.rows, row = r % p.rows.rows;
         const Out &out = j < NP ? o.Bb : o.Cb;

@@ -27,9 +27,21 @@ template <class T> int scan_backward_channels(int n)
 {
     return with_states(n, [](auto np) { return ScanBwdTile<T, np.value>::CW; });
 }
-template <class T> cudaError_t scan_launch(const ScanArgs &p, cudaStream_t s)
+template <class T> cudaError_t scan_launch(const ScanArgs &p, int lanes, cudaStream_t s)
 {
-    return with_states(p.n, [&](auto np) { return scan_run<T, np.value>(p, s); });
+    return with_states(p.n, [&](auto np) {
+        constexpr int NP = np.value;
+        if constexpr (NP <= 16) {
+            if (lanes == 1) return scan_run<ScanFwdTile<T, NP, 1>>(p, s);
+        }
+        if constexpr (NP == 8 || NP == 16 || NP == 32) {
+            if (lanes == 2) return scan_run<ScanFwdTile<T, NP, 2>>(p, s);
+        }
+        if constexpr (NP >= 16) {
+            if (lanes == 4) return scan_run<ScanFwdTile<T, NP, 4>>(p, s);
+        }
+        return cudaErrorInvalidValue;
+    });
 }
 template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, cudaStream_t s)
 {
@@ -46,7 +58,7 @@ template <class T> cudaError_t scan_step_launch(const ScanStepArgs &p, cudaStrea
 
 #define SELINV_SCAN_INSTANCES(T)                                                                   \
     template int scan_backward_channels<T>(int);                                                   \
-    template cudaError_t scan_launch<T>(const ScanArgs &, cudaStream_t);                           \
+    template cudaError_t scan_launch<T>(const ScanArgs &, int, cudaStream_t);                      \
     template cudaError_t scan_backward_launch<T>(const ScanArgs &, const ScanGrads &, cudaStream_t); \
     template cudaError_t scan_step_launch<T>(const ScanStepArgs &, cudaStream_t);
 

@@ -5,10 +5,12 @@
 
 namespace selinv {
 
-// States are padded to 4, 8, 16, 32 or 64.  Channels of a warp: 32 in the forward.
-constexpr int SCAN_FORWARD_CHANNELS = 32;
+// States are padded to 4, 8, 16, 32 or 64.  In the forward 1, 2 or 4 lanes share a channel, none with more than 16
+// states or fewer than 4; a warp has 32 / lanes channels.
+constexpr int scan_least_lanes(int n) { return n <= 16 ? 1 : n <= 32 ? 2 : 4; }
+constexpr int scan_most_lanes(int n) { return n <= 4 ? 1 : n <= 8 ? 2 : 4; }
 template <class T> int scan_backward_channels(int n);
-template <class T> cudaError_t scan_launch(const ScanArgs &p, cudaStream_t s);
+template <class T> cudaError_t scan_launch(const ScanArgs &p, int lanes, cudaStream_t s);
 template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, cudaStream_t s);
 template <class T> cudaError_t scan_step_launch(const ScanStepArgs &p, cudaStream_t s);
 template <class T> cudaError_t conv_launch(const ConvArgs &p, cudaStream_t s);
