@@ -9,7 +9,7 @@ using namespace selinv;
 
 namespace {
 
-constexpr int64_t MAX_D = 1 << 20, MAX_ROWS = 0x7fffffff - 64, MAX_STRIDE = 0x7fffffff, MAX_GRID_X = 0x7fffffff, MAX_GRID_Y = 65535;
+constexpr int64_t MAX_D = 1 << 20, MAX_ROWS = 0x7fffffff - 64, MAX_STRIDE = 0x7fffffff, MAX_SEGS = 160, MAX_GRID_X = 0x7fffffff, MAX_GRID_Y = 65535;
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -102,12 +102,27 @@ Spread scan_spread(const selinv_scan_inputs &a, bool backward)
     const auto blocks = [&](int64_t channels) { return lines * a.groups * div_up(div_up(per, channels), SCAN_BLOCK_TILES); };
     Spread s{scan_least_lanes(n), 1, a.rows, 0, 0};
     int64_t cw = backward ? with_type(a.dtype, [&](auto t) { return scan_backward_channels<decltype(t)>(n); }) : 32 / s.lanes;
+    // A line that is cut is run twice but for its last segment, first for the states that segments leave behind.  So it
+    // is cut only where the blocks do not come to about one per SM (forward; 128 blocks of 4 x 2048 x 4096 x 16 take 354
+    // us whole, 350 in 16 segments) or one and a half (backward, whose second run costs less: 128 blocks 1297 and 994
+    // us, 256 blocks 895 and 965).
+    if (blocks(cw) * 10 < (backward ? 15 : 8) * sms) {
+        const int64_t resident = (backward ? 2 : 4) * sms;
+        // more lanes per channel where segments alone do not fill the GPU (1 x 300 x 1024 x 16: 35 us with one, 27 with four)
+        if (!backward)
+            while (s.lanes < scan_most_lanes(n) && blocks(cw) * (a.rows / 64 > 1 ? a.rows / 64 : 1) < 3 * sms)
+                s.lanes *= 2, cw /= 2;
+        // As many segments as are resident at once, or where that leaves SMs with fewer than the others, so many that they
+        // end together (128 blocks forward: 409 us in 4 segments, 352 in 8); none under 64 rows unless SMs would be idle.
+        const int64_t b = blocks(cw);
+        int64_t segs = resident / b;
+        if (segs * b * 100 < 93 * resident) segs = 7 * sms / b;
+        if (segs > a.rows / 64) segs = a.rows / 64;
+        if (b * segs < 2 * sms) segs = 2 * sms / b < a.rows / 32 ? 2 * sms / b : a.rows / 32;
+        s.segs = (int)(segs < 1 ? 1 : segs < MAX_SEGS ? segs : MAX_SEGS);
+    }
     s.tiles = a.groups * div_up(per, cw);
     s.blocks = a.groups * div_up(div_up(per, cw), SCAN_BLOCK_TILES);
-    // Lines are cut where their blocks do not fill the GPU: into so many segments that all are resident at once (four
-    // blocks per SM forward, two backward), none under 64 rows.
-    const int64_t room = (backward ? 2 : 4) * sms / (lines * s.blocks), most = a.rows / 64 > 1 ? a.rows / 64 : 1;
-    s.segs = (int)(room < 2 ? 1 : room < most ? room : most);
     s.seg_rows = div_up(div_up(a.rows, s.segs), SCAN_KEEP_ROWS) * SCAN_KEEP_ROWS;
     if (s.seg_rows < SCAN_KEEP_ROWS) s.seg_rows = SCAN_KEEP_ROWS;
     s.segs = (int)div_up(a.rows, s.seg_rows);

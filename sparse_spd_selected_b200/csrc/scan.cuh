@@ -124,7 +124,8 @@ SELINV_DEVINL void raw_prefetch(const T *from, int stride, int r, int r1, int nc
     if (lane < SCAN_R && r + lane < r1 && nch > 0) prefetch_l2(from + (int64_t)(r + lane) * stride);
 }
 // The same of B or C [rows, n] into rows of NP, dealt out over THREADS threads; with zeros where states or rows are not
-// there (they take part in sums over channels).
+// there (they take part in sums over channels).  FULL: all rows, whole vectors; the states that are not there are zero
+// already (raw_clear_n).
 template <int THREADS, bool FULL, class T, int NP>
 SELINV_DEVINL void raw_fetch_n(T (*to)[NP], const T *from, int stride, int r, int r1, int n, bool wide, int thread)
 {
@@ -134,18 +135,25 @@ SELINV_DEVINL void raw_fetch_n(T (*to)[NP], const T *from, int stride, int r, in
     for (int i = thread; i < SCAN_R * ROW; i += THREADS) {
         const int row = i / ROW, e = (i % ROW) * E;
         const T *at = from + ((int64_t)(r + row) * stride + e);
-        if (FULL || (wide && row < nr && e + E <= n)) {
+        if (FULL ? NP == n || e < n : (wide && row < nr && e + E <= n)) {
             if constexpr (sizeof(T) == 2)
                 cp_async8(&to[row][e], at);
             else
                 cp_async16(&to[row][e], at);
-        } else {
+        } else if (!FULL) {
 #pragma unroll
             for (int q = 0; q < E; ++q)
                 to[row][e + q] = row < nr && e + q < n ? at[q] : Elem<T>::down((typename Elem<T>::C)0);
         }
     }
 }
+template <int THREADS, class T, int NP> SELINV_DEVINL void raw_clear_n(T (*to)[NP], int n, int thread)
+{
+    if (n == NP) return;
+    for (int i = thread; i < SCAN_R * NP; i += THREADS) to[i / NP][i % NP] = Elem<T>::down((typename Elem<T>::C)0);
+}
+// Whether B's and C's states come in whole vectors.
+template <class T> SELINV_DEVINL bool whole_n(int n) { return n % (sizeof(T) == 2 ? 4 : 16 / (int)sizeof(T)) == 0; }
 // From there into the arithmetic type.
 template <int THREADS, class T, int NP>
 SELINV_DEVINL void raw_stage_n(typename Elem<T>::C (*to)[NP], const T (*from)[NP], int thread)

@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
                 if (r + LN * i < rows) out[i].store(to + (int64_t)(LN * i) * stride, have, false);
         }
     };
-    const bool full = p.x.wide && p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.B.wide && p.C.wide && w.nch == CW && n == NP;
+    const bool full = p.x.wide && p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.B.wide && p.C.wide && w.nch == CW && whole_n<T>(n);
     auto fetch_as = [&](auto whole, int r) {
         constexpr bool F = whole.value;
         raw_fetch<CW, F>(sm.x, x, p.x.row, r, w.r1, w.nch, p.x.wide, lane);
@@ -328,6 +328,9 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
         else
             fetch_as(std::false_type(), r);
     };
+    raw_clear_n<SCAN_WARPS * 32>(block.b_raw, n, threadIdx.x);
+    raw_clear_n<SCAN_WARPS * 32>(block.c_raw, n, threadIdx.x);
+    __syncthreads();
     int rt = w.r0 + (w.r1 > w.r0 ? (w.r1 - w.r0 - 1) / R * R : 0);
     if (w.r1 > w.r0) fetch(rt);
     for (; rt >= w.r0 && rt < w.r1; rt -= R) {
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
     zero_states<NP>(g);
     const C bias = in && p.dt_bias ? static_cast<const C *>(p.dt_bias)[w.c0 + lane] : (C)0;
     C total = 0;
-    const bool full = p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.C.wide && w.nch == 32 && n == NP;
+    const bool full = p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.C.wide && w.nch == 32 && whole_n<T>(n);
     auto fetch_as = [&](auto whole, int r, int to) {
         constexpr bool F = whole.value;
         raw_fetch<32, F>(sm.raw[to].dt, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
@@ -557,6 +560,9 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
         else
             fetch_as(std::false_type(), r, to);
     };
+    raw_clear_n<32>(sm.raw[0].c, n, lane);
+    raw_clear_n<32>(sm.raw[1].c, n, lane);
+    __syncwarp();
     int k = p.rows.find(w.r1 - 1);          // the sequence of the row at hand
     int rt = w.r0 + (w.r1 - w.r0 - 1) / R * R, now = 0;
     fetch(rt, 0);

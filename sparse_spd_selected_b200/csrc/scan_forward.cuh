@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) scan_kernel(const __grid_cons
         scan_join<SN, C>(p, w.line, p.rows.start(k) / p.seg_rows, w.seg, 1, w.c0 + dl, own, n, in, A2, h);
     }
 
-    const bool full = p.x.wide && p.dt.wide && (!z || p.z.wide) && p.B.wide && p.C.wide && w.nch == CW && p.n == K::NP;
+    const bool full = p.x.wide && p.dt.wide && (!z || p.z.wide) && p.B.wide && p.C.wide && w.nch == CW && whole_n<T>(p.n);
     auto fetch_as = [&](auto whole, int r, int to) {
         constexpr bool F = whole.value;
         raw_fetch<CW, F>(sm.raw[to].x, x, p.x.row, r, w.r1, w.nch, p.x.wide, lane);
@@ -125,6 +125,12 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) scan_kernel(const __grid_cons
         else
             fetch_as(std::false_type(), r, to);
     };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        raw_clear_n<32>(sm.raw[i].b, p.n, lane);
+        if (MAIN) raw_clear_n<32>(sm.raw[i].c, p.n, lane);
+    }
+    __syncwarp();
     fetch(w.r0, 0);
     C total = 0;
 

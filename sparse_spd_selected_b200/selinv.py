@@ -993,10 +993,10 @@ def _arith(dtype):
 
 
 def _element_code(name, t) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    code = _ELEMENTS.get(t.dtype)
+    code = _ELEMENTS.get(t.dtype) if isinstance(t, torch.Tensor) and t.is_cuda else None
     if code is None:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
         raise TypeError(f"{name} must be float64, float32, bfloat16 or float16, not {t.dtype}")
     return code
 
@@ -1005,24 +1005,28 @@ def _like(name, t, dtype, device, shape, contiguous=True):
     """Checks a tensor's type, device and shape; returns its address (0 for None)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or t.device != device:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype is dtype and t.shape == shape and t.device == device and (not contiguous or t.is_contiguous()):
+        return t.data_ptr()
+    if t.device != device:
         raise ValueError(f"{name} must be a tensor on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _view(name, t, inner, output=False):
     """(address, stride between lines, stride between rows) of a tensor [..., rows, *inner dims]: its last dimension
     contiguous, its leading dimensions one even stride apart."""
-    if t.numel() == 0:
-        return t.data_ptr(), 0, 0
     st, sh = t.stride(), t.shape
     at = len(sh) - 1 - inner
+    if at == 0 and st[-1] == 1 and not output:
+        return t.data_ptr(), 0, st[0]
+    if 0 in sh:
+        return t.data_ptr(), 0, 0
     if st[-1] != 1 and sh[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     line = 0
@@ -1035,7 +1039,7 @@ def _view(name, t, inner, output=False):
             size *= sh[i]
         else:
             raise ValueError(f"{name}'s leading dimensions must be evenly strided")
-    if output and t.numel() > 0:
+    if output:
         need = 1
         for size, stride in sorted(((n, v) for n, v in zip(sh, st) if n > 1), key=lambda e: e[1]):
             if stride < need:
@@ -1265,8 +1269,10 @@ def _step_slots(cache, shape, batch, index, cache_out, check, dev):
     slots = cache.shape[0]
     if cache_out is None:
         cache_out = cache
-    elif cache_out.data_ptr() != cache.data_ptr() or cache_out.shape != cache.shape:
-        _apart("cache_out", cache_out, (("cache", cache),))
+    else:
+        gap = cache_out.data_ptr() - cache.data_ptr()       # both contiguous, of one shape and type (checked below)
+        if gap and -cache_out.nbytes < gap < cache.nbytes:
+            raise ValueError("cache_out must be cache or not overlap it")
     info = None
     if index is None:
         if slots < batch:
@@ -1298,10 +1304,14 @@ def causal_conv_step(cache, x, weight, bias=None, *, silu=False, index=None, cac
         raise ValueError("x must be [batch, d] and weight [d, k]")
     (batch, d), k = x.shape, weight.shape[1]
     slots, new, at, info = _step_slots(cache, (k - 1, d), batch, index, cache_out, check, dev)
-    given = (("x", x), ("weight", weight), ("bias", bias), ("cache", cache), ("cache_out", new)) if out else ()
-    y = _output(out, "y", (batch, d), dt, dev, None, given)
+    if out:
+        given = (("x", x), ("weight", weight), ("bias", bias), ("cache", cache), ("cache_out", new))
+        y = _output(out, "y", (batch, d), dt, dev, None, given)
+        yp, _, y_row = _view("y", y, 1, True)
+    else:
+        y = x.new_empty((batch, d))
+        yp, y_row = y.data_ptr(), d
     xp, _, x_row = _view("x", x, 1)
-    yp, _, y_row = _view("y", y, 1, out is not None)
     packed = _CONV_STEP.pack(code, _SILU if silu else 0, batch, slots, d, k, xp, _like("weight", weight, dt, dev, (d, k)),
                              _like("bias", bias, dt, dev, (d,)), _like("cache", cache, dt, dev, (slots, k - 1, d)),
                              x_row, y_row, _like("cache_out", new, dt, dev, (slots, k - 1, d)), yp, at,
@@ -1453,14 +1463,17 @@ def selective_scan_step(cache, x, dt, A, B, C, D=None, *, z=None, dt_bias=None, 
     _like("B", B, ty, dev, bc, False)
     _like("C", C, ty, dev, bc, False)
     slots, new, at, info = _step_slots(cache, (d, n), batch, index, cache_out, check, dev)
-    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, cache, ("cache_out", new)) if out else ()
-    y = _output(out, "y", (batch, d), ty, dev, None, given)
+    if out:
+        y = _output(out, "y", (batch, d), ty, dev, None, _scan_given(x, dt, A, B, C, D, z, dt_bias, cache, ("cache_out", new)))
+        yp, _, y_row = _view("y", y, 1, True)
+    else:
+        y = x.new_empty((batch, d))
+        yp, y_row = y.data_ptr(), d
     xp, _, x_row = _view("x", x, 1)
     dp, _, d_row = _view("dt", dt, 1)
     zp, _, z_row = (0, 0, 0) if z is None else _view("z", z, 1)
     bp, _, b_row = _view("B", B, 2)
     cp, _, c_row = _view("C", C, 2)
-    yp, _, y_row = _view("y", y, 1, out is not None)
     packed = _SCAN_STEP.pack(code, _SOFTPLUS if softplus else 0, batch, slots, d, n, groups, xp, dp, zp, bp, cp,
                              x_row, d_row, z_row, b_row, c_row, B.stride(1), C.stride(1), y_row,
                              _like("A", A, ct, dev, (d, n)), _like("D", D, ct, dev, (d,)),
