@@ -342,7 +342,7 @@ selinv_status selinv_selective_scan_step(const selinv_scan_step *a, void *stream
     if (a->x_row < 0 || a->dt_row < 0 || a->z_row < 0 || a->B_row < 0 || a->C_row < 0 || a->B_group < 0 || a->C_group < 0 ||
         a->y_row < 0)
         return SELINV_ERR_INVALID_ARG;
-    if (a->batch * div_up(a->d, 256 / (scan_padded((int)a->n) / 4)) > MAX_GRID_X) return SELINV_ERR_UNSUPPORTED;
+    if (a->batch * div_up(a->d, 128) > MAX_GRID_X) return SELINV_ERR_UNSUPPORTED;
     ScanStepArgs p{};
     p.batch = a->batch, p.d = a->d, p.slots = a->slots, p.n = (int)a->n, p.groups = (int)a->groups;
     p.softplus = a->flags & SELINV_SOFTPLUS;

@@ -391,20 +391,25 @@ template <class C> __global__ void __launch_bounds__(256) conv_params_kernel(con
     }
 }
 
-// What a step does with row r: its slot, or -1 where it leaves the cache alone.  A slot of -1 skips the row; one
-// outside the cache, or one that an earlier row names too, is reported.  Every thread of the block calls it.
-SELINV_DEVINL int64_t step_slot(const int32_t *index, int32_t *info, int64_t r, int64_t slots, bool reports)
+// The slot of a step's row r, or -1 where there is none: a slot of -1 skips the row, one outside the cache is reported.
+SELINV_DEVINL int64_t step_slot(const int32_t *index, int64_t r, int64_t slots)
 {
     if (!index) return r;
     const int32_t slot = index[r];
-    int32_t status = STEP_OK;
+    return slot >= 0 && slot < slots ? slot : -1;
+}
+// Whether the row may write to it: no earlier row names the same slot.  Reports the row's status.  Every thread of the
+// block calls it, once its loads are on their way.
+SELINV_DEVINL bool step_first(const int32_t *index, int32_t *info, int64_t r, int64_t slot, bool reports)
+{
+    if (!index) return true;
     bool twice = false;
-    if (slot < -1 || slot >= slots) status = STEP_RANGE;
     if (slot >= 0)
         for (int64_t i = threadIdx.x; i < r; i += blockDim.x) twice |= index[i] == slot;
-    if (__syncthreads_or(twice)) status = STEP_TWICE;
-    if (reports && info && threadIdx.x == 0) info[r] = status;
-    return status == STEP_OK ? slot : -1;
+    twice = __syncthreads_or(twice);
+    if (reports && info && threadIdx.x == 0)
+        info[r] = twice ? STEP_TWICE : slot < 0 && index[r] != -1 ? STEP_RANGE : STEP_OK;
+    return slot >= 0 && !twice;
 }
 
 // One row per sequence over a cache of states [slots, K - 1, d].
@@ -414,26 +419,36 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_step_kernel(const __grid_co
     using C = typename Elem<T>::C;
     const int64_t blocks = (p.d + CONV_THREADS - 1) / CONV_THREADS, r = blockIdx.x / blocks;
     const int64_t c = (blockIdx.x % blocks) * CONV_THREADS + threadIdx.x;
-    const int64_t slot = step_slot(p.index, p.info, r, p.slots, blockIdx.x % blocks == 0);
-    if (c >= p.d) return;
-    T *y = static_cast<T *>(p.y) + r * p.y_row + c;
-    if (slot < 0) {
-        *y = Elem<T>::down((C)0);
-        return;
-    }
-    const T *in = static_cast<const T *>(p.cache) + slot * (K - 1) * p.d + c;
-    T *out = static_cast<T *>(p.cache_out) + slot * (K - 1) * p.d + c;
+    const int64_t slot = step_slot(p.index, r, p.slots);
+    const bool in = c < p.d;
     T win[K];
+    C wt[K], bias = 0;
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) win[j] = in[j * p.d];
-    win[K - 1] = static_cast<const T *>(p.x)[r * p.x_row + c];
-    C v = p.bias ? Elem<T>::up(static_cast<const T *>(p.bias)[c]) : (C)0;
+    for (int j = 0; j < K; ++j) {
+        win[j] = Elem<T>::down((C)0);
+        wt[j] = 0;
+    }
+    if (in && slot >= 0) {
+        const T *at = static_cast<const T *>(p.cache) + slot * (K - 1) * p.d + c;
 #pragma unroll
-    for (int j = 0; j < K; ++j) v += Elem<T>::up(static_cast<const T *>(p.weight)[c * K + j]) * Elem<T>::up(win[j]);
+        for (int j = 0; j < K - 1; ++j) win[j] = at[j * p.d];
+        win[K - 1] = static_cast<const T *>(p.x)[r * p.x_row + c];
+        if (p.bias) bias = Elem<T>::up(static_cast<const T *>(p.bias)[c]);
+#pragma unroll
+        for (int j = 0; j < K; ++j) wt[j] = Elem<T>::up(static_cast<const T *>(p.weight)[c * K + j]);
+    }
+    const bool ours = step_first(p.index, p.info, r, slot, blockIdx.x % blocks == 0);
+    if (!in) return;
+    C v = bias;
+#pragma unroll
+    for (int j = 0; j < K; ++j) v += wt[j] * Elem<T>::up(win[j]);
     if (p.silu) v *= sigmoid_(v);
-    *y = Elem<T>::down(v);
+    static_cast<T *>(p.y)[r * p.y_row + c] = Elem<T>::down(ours ? v : (C)0);
+    if (ours) {
+        T *out = static_cast<T *>(p.cache_out) + slot * (K - 1) * p.d + c;
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) out[j * p.d] = win[j + 1];
+        for (int j = 0; j < K - 1; ++j) out[j * p.d] = win[j + 1];
+    }
 }
 
 template <class T, int K> cudaError_t conv_run(const ConvArgs &p, cudaStream_t s)

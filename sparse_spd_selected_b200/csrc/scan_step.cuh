@@ -1,7 +1,9 @@
 // The selective scan for single tokens: one row per sequence over a cache of
-// states [slots, d, n].  Bounded by memory, the states read and written once:
-// a thread takes four neighbouring states of one channel, the LN lanes of a
-// channel add their parts of y.
+// states [slots, d, n].  Bounded by memory, the states read and written once.
+// Each lane has a channel of its own for what a channel has once (step, gate,
+// y); for the states LN neighbouring lanes take their LN channels one after
+// another, four states of each a lane, so that the loads and stores of 16
+// bytes cover whole sectors.
 #pragma once
 
 #include "conv.cuh"
@@ -10,78 +12,109 @@
 namespace selinv {
 namespace {
 
-constexpr int STEP_THREADS = 256;
+constexpr int STEP_THREADS = 128;
 
 template <class T, int LN>
 __global__ void __launch_bounds__(STEP_THREADS) scan_step_kernel(const __grid_constant__ ScanStepArgs p)
 {
     using C = typename Elem<T>::C;
-    constexpr int CH = STEP_THREADS / LN;
-    const int64_t blocks = (p.d + CH - 1) / CH, r = blockIdx.x / blocks;
-    const int64_t c = (blockIdx.x % blocks) * CH + threadIdx.x / LN;
-    const int64_t slot = step_slot(p.index, p.info, r, p.slots, blockIdx.x % blocks == 0);
-    const int lane = threadIdx.x % 32, n0 = (threadIdx.x % LN) * 4, n = p.n;
-    const bool in = c < p.d;
+    const int blocks = (int)((p.d + STEP_THREADS - 1) / STEP_THREADS), bi = (int)(blockIdx.x % blocks);
+    const int64_t r = blockIdx.x / blocks;
+    const int64_t slot = step_slot(p.index, r, p.slots);
+    const int lane = threadIdx.x % 32, nl = threadIdx.x % LN, n0 = nl * 4, n = p.n, d = (int)p.d;
+    const int c = bi * STEP_THREADS + threadIdx.x, first = c - nl;      // this lane's channel, and its lanes' first
+    const bool in = c < d;
+    const bool wide = n % 4 == 0 && sizeof(C) == 4 &&
+                      ((uintptr_t)p.cache | (uintptr_t)p.cache_out | (uintptr_t)p.A) % 16 == 0;
+    constexpr int U = LN < 4 ? LN : 4;          // channels whose loads are on their way together
+    C h[U][4], a[U][4];
+    const auto load = [&](int u0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int ch = first + u0 + u;
+            const C *hs = static_cast<const C *>(p.cache) + (slot * d + ch) * n + n0;
+            const C *as = static_cast<const C *>(p.A) + (int64_t)ch * n + n0;
+            const bool have = slot >= 0 && ch < d && n0 < n;
+            if (have && wide) {
+                get<4>(hs, h[u]);
+                get<4>(as, a[u]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h[u][j] = have && n0 + j < n ? hs[j] : (C)0;
+                    a[u][j] = have && n0 + j < n ? as[j] : (C)0;
+                }
+            }
+        }
+    };
+    load(0);
+    C x = 0, dt = 0, z = 0, skip = 0;
+    if (in) {
+        x = Elem<T>::up(static_cast<const T *>(p.x)[r * p.x_row + c]);
+        dt = Elem<T>::up(static_cast<const T *>(p.dt)[r * p.dt_row + c]);
+        if (p.dt_bias) dt += static_cast<const C *>(p.dt_bias)[c];
+        if (p.z) z = Elem<T>::up(static_cast<const T *>(p.z)[r * p.z_row + c]);
+        if (p.D) skip = static_cast<const C *>(p.D)[c];
+    }
+    const bool ours = step_first(p.index, p.info, r, slot, bi == 0);
     T *y = static_cast<T *>(p.y) + r * p.y_row + c;
-    if (slot < 0) {
-        if (in && threadIdx.x % LN == 0) *y = Elem<T>::down((C)0);
+    if (!ours) {
+        if (in) *y = Elem<T>::down((C)0);
         return;
     }
-    C v[1] = {0}, x = 0;
-    if (in) {
-        const int64_t at = (slot * p.d + c) * n + n0, g = c / (p.d / p.groups);
-        const C *h = static_cast<const C *>(p.cache) + at, *A = static_cast<const C *>(p.A) + c * n + n0;
-        C *out = static_cast<C *>(p.cache_out) + at;
-        const T *B = static_cast<const T *>(p.B) + r * p.B_row + g * p.B_group + n0;
-        const T *Cc = static_cast<const T *>(p.C) + r * p.C_row + g * p.C_group + n0;
-        C hs[4], as[4];
-        const bool wide = n % 4 == 0 && sizeof(C) == 4 &&
-                          ((uintptr_t)p.cache | (uintptr_t)p.cache_out | (uintptr_t)p.A) % 16 == 0;
-        if (wide && n0 < n) {
-            get<4>(h, hs);
-            get<4>(A, as);
-        } else {
+    const int per = d / p.groups;
+    C b[4], cc[4], v[LN];
+    int group = -1;
+    if (p.softplus) dt = softplus_(dt);
+    const C ux = dt * x, d2 = dt * log2e<C>();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                hs[j] = n0 + j < n ? h[j] : (C)0;
-                as[j] = n0 + j < n ? A[j] : (C)0;
-            }
-        }
-        x = Elem<T>::up(static_cast<const T *>(p.x)[r * p.x_row + c]);
-        C dt = Elem<T>::up(static_cast<const T *>(p.dt)[r * p.dt_row + c]);
-        if (p.dt_bias) dt += static_cast<const C *>(p.dt_bias)[c];
-        if (p.softplus) dt = softplus_(dt);
-        const C u = dt * x, d2 = dt * log2e<C>();
+    for (int u0 = 0; u0 < LN; u0 += U) {
+        if (u0) load(u0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (n0 + j < n) {
-                hs[j] = exp2_(d2 * as[j]) * hs[j] + u * Elem<T>::up(B[j]);
-                v[0] += Elem<T>::up(Cc[j]) * hs[j];
+        for (int u = 0; u < U; ++u) {
+            const int ch = first + u0 + u, from = lane - nl + u0 + u;
+            const int g = ch < d ? ch / per : group;
+            if (g != group) {       // once in a call with one group
+                group = g;
+                const T *B = static_cast<const T *>(p.B) + r * p.B_row + g * p.B_group + n0;
+                const T *Cc = static_cast<const T *>(p.C) + r * p.C_row + g * p.C_group + n0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    b[j] = n0 + j < n ? Elem<T>::up(B[j]) : (C)0;
+                    cc[j] = n0 + j < n ? Elem<T>::up(Cc[j]) : (C)0;
+                }
             }
-        if (wide && n0 < n) {
-            put<4>(out, hs);
-        } else {
+            const C e = LN > 1 ? __shfl_sync(FULL_MASK, d2, from) : d2, w = LN > 1 ? __shfl_sync(FULL_MASK, ux, from) : ux;
+            v[u0 + u] = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (n0 + j < n) out[j] = hs[j];
+                if (n0 + j < n) {
+                    h[u][j] = exp2_(e * a[u][j]) * h[u][j] + w * b[j];
+                    v[u0 + u] += cc[j] * h[u][j];
+                }
+            if (ch < d && n0 < n) {
+                C *out = static_cast<C *>(p.cache_out) + (slot * d + ch) * n + n0;
+                if (wide) {
+                    put<4>(out, h[u]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (n0 + j < n) out[j] = h[u][j];
+                }
+            }
         }
     }
-    scatter_sum<1, 1, LN>(v, lane);
-    if (in && threadIdx.x % LN == 0) {
-        C t = v[0];
-        if (p.D) t += static_cast<const C *>(p.D)[c] * x;
-        if (p.z) {
-            const C z = Elem<T>::up(static_cast<const T *>(p.z)[r * p.z_row + c]);
-            t *= z * sigmoid_(z);
-        }
+    scatter_sum<LN, 1, LN>(v, lane);        // each lane ends with its own channel's sum
+    if (in) {
+        C t = v[0] + skip * x;
+        if (p.z) t *= z * sigmoid_(z);
         *y = Elem<T>::down(t);
     }
 }
 
 template <class T, int LN> cudaError_t scan_step_run(const ScanStepArgs &p, cudaStream_t s)
 {
-    constexpr int CH = STEP_THREADS / LN;
-    const int64_t blocks = (p.d + CH - 1) / CH * p.batch;
+    const int64_t blocks = (p.d + STEP_THREADS - 1) / STEP_THREADS * p.batch;
     scan_step_kernel<T, LN><<<(unsigned)blocks, STEP_THREADS, 0, s>>>(p);
     return cudaGetLastError();
 }
