@@ -224,7 +224,7 @@ SELINV_DEVINL void scan_join(const ScanArgs &p, int64_t line, int s, int to, int
         load_states<N>(ends + s * dn, m, in, e);
         const C t = in ? sums[s * p.d] : (C)0;
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) h[j] = fma2(exp2_2(mul2(make2(t, t), A2[j])), h[j], e[j]);
+        for (int j = 0; j < N / 2; ++j) h[j] = fma2(decay2(make2(t, t), A2[j]), h[j], e[j]);
     }
 }
 

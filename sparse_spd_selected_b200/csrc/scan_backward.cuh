@@ -104,8 +104,8 @@ template <class K> struct ScanBwd {
         const V u = mul2(dt, x), d0 = make2(dt.x, dt.x), d1 = make2(dt.y, dt.y), u0 = make2(u.x, u.x), u1 = make2(u.y, u.y);
 #pragma unroll
         for (int j = 0; j < KP; ++j) {
-            a[0][j] = exp2_2(mul2(d0, A2[0][j]));
-            a[1][j] = exp2_2(mul2(d1, A2[1][j]));
+            a[0][j] = decay2(d0, A2[0][j]);
+            a[1][j] = decay2(d1, A2[1][j]);
             h[0][j] = fma2(a[0][j], h[0][j], mul2(u0, b[j]));
             h[1][j] = fma2(a[1][j], h[1][j], mul2(u1, b[j]));
         }
@@ -516,7 +516,7 @@ SELINV_DEVINL void scan_ends_row(const ScanEndsSmem<T, NP> &sm, int t, int lane,
         V c[2];
         get<2>(&sm.c[t][2 * j], c);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) g[j + i] = mul2(exp2_2(mul2(d2, A2[j + i])), fma2(c[i], y2, g[j + i]));
+        for (int i = 0; i < 2; ++i) g[j + i] = mul2(decay2(d2, A2[j + i]), fma2(c[i], y2, g[j + i]));
     }
 }
 template <class T, int NP>

@@ -51,7 +51,7 @@ SELINV_DEVINL typename K::C scan_row(const ScanFwdSmem<K> &sm, int t, int dl, in
         if (MAIN) get<2>(&sm.c[t][n0 + 2 * j], c);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            h[j + i] = fma2(exp2_2(mul2(dt2, A2[j + i])), h[j + i], mul2(u2, b[i]));
+            h[j + i] = fma2(decay2(dt2, A2[j + i]), h[j + i], mul2(u2, b[i]));
             if (MAIN) y[i] = fma2(c[i], h[j + i], y[i]);
         }
     }
