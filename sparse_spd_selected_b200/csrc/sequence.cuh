@@ -32,11 +32,40 @@ template <> struct Elem<double> {
 };
 template <> struct Elem<__nv_bfloat16> {
     using C = float;
+    // two elements of a word, and back: one instruction
+    SELINV_DEVINL static float low(uint32_t w) { return __uint_as_float(w << 16); }
+    SELINV_DEVINL static float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+    SELINV_DEVINL static uint32_t pair(float a, float b)
+    {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        uint32_t w;
+        memcpy(&w, &v, 4);
+        return w;
+    }
     SELINV_DEVINL static float up(__nv_bfloat16 v) { return __bfloat162float(v); }
     SELINV_DEVINL static __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
 };
 template <> struct Elem<__half> {
     using C = float;
+    SELINV_DEVINL static float low(uint32_t w)
+    {
+        __half2 v;
+        memcpy(&v, &w, 4);
+        return __low2float(v);
+    }
+    SELINV_DEVINL static float high(uint32_t w)
+    {
+        __half2 v;
+        memcpy(&v, &w, 4);
+        return __high2float(v);
+    }
+    SELINV_DEVINL static uint32_t pair(float a, float b)
+    {
+        const __half2 v = __floats2half2_rn(a, b);
+        uint32_t w;
+        memcpy(&w, &v, 4);
+        return w;
+    }
     SELINV_DEVINL static float up(__half v) { return __half2float(v); }
     SELINV_DEVINL static __half down(float v) { return __float2half_rn(v); }
 };
@@ -55,11 +84,7 @@ template <class T, int E> struct Pack {
     SELINV_DEVINL typename Elem<T>::C get(int e) const
     {
         if constexpr (sizeof(T) == 2) {
-            const uint32_t v = w[e >> 1];
-            const unsigned short h = (e & 1) ? (unsigned short)(v >> 16) : (unsigned short)(v & 0xffffu);
-            T t;
-            memcpy(&t, &h, 2);
-            return Elem<T>::up(t);
+            return e & 1 ? Elem<T>::high(w[e >> 1]) : Elem<T>::low(w[e >> 1]);
         } else if constexpr (sizeof(T) == 4) {
             return __uint_as_float(w[e]);
         } else {
@@ -71,13 +96,7 @@ template <class T, int E> struct Pack {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             if constexpr (sizeof(T) == 2) {
-                const T t = Elem<T>::down(v[e]);
-                unsigned short h;
-                memcpy(&h, &t, 2);
-                if (e & 1)
-                    w[e >> 1] |= (uint32_t)h << 16;
-                else
-                    w[e >> 1] = h;
+                if (e % 2 == 0) w[e / 2] = Elem<T>::pair(v[e], v[e + 1]);
             } else if constexpr (sizeof(T) == 4) {
                 w[e] = __float_as_uint(v[e]);
             } else {
