@@ -103,11 +103,12 @@ Spread scan_spread(const selinv_scan_inputs &a, bool backward)
     Spread s{scan_least_lanes(n), 1, a.rows, 0, 0};
     int64_t cw = backward ? with_type(a.dtype, [&](auto t) { return scan_backward_channels<decltype(t)>(n); }) : 32 / s.lanes;
     // A line that is cut is run twice but for its last segment, first for the states that segments leave behind.  So it
-    // is cut only where the blocks do not come to about one per SM (forward; 128 blocks of 4 x 2048 x 4096 x 16 take 354
-    // us whole, 350 in 16 segments) or one and a half (backward, whose second run costs less: 128 blocks 1297 and 994
-    // us, 256 blocks 895 and 965).
-    if (blocks(cw) * 10 < (backward ? 15 : 8) * sms) {
-        const int64_t resident = (backward ? 2 : 4) * sms;
+    // is cut only where its blocks come to less than about one per SM (forward; 128 blocks of 4 x 2048 x 4096 x 16 take
+    // 354 us whole, 350 in 16 segments) or to less than 0.7 of those resident (backward; with two resident per SM 128
+    // blocks take 1297 us whole and 994 in 8 segments, 256 blocks 895 whole and 965 in 4).
+    const int64_t resident =
+        (backward ? with_type(a.dtype, [&](auto t) { return scan_backward_blocks<decltype(t)>(n); }) : 4) * sms;
+    if (blocks(cw) * 10 < (backward ? 7 * resident : 8 * sms)) {
         // more lanes per channel where segments alone do not fill the GPU (1 x 300 x 1024 x 16: 35 us with one, 27 with four)
         if (!backward)
             while (s.lanes < scan_most_lanes(n) && blocks(cw) * (a.rows / 64 > 1 ? a.rows / 64 : 1) < 3 * sms)

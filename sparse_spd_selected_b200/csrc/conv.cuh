@@ -378,6 +378,7 @@ template <class C> __global__ void __launch_bounds__(256) conv_params_kernel(con
     const int j = blockIdx.y, strand = threadIdx.x / 32;
     C v = 0;
     if (c < p.d)
+#pragma unroll 8
         for (int64_t i = strand; i < count; i += 8)
             v += static_cast<const C *>(p.part)[(i * (p.k + 1) + j) * p.d + c];
     s[strand][threadIdx.x % 32] = v;

@@ -5,7 +5,8 @@
 //   xb = dt' (g . B) + D yb'        dt'b = x (g . B) + q . A     Ab = sum_t q dt'
 //   Bb = sum_d g dt' x              Cb = sum_d h yb'             Db = sum_t yb' x
 //   zb = yb silu'(z) (h . C + D x)  dtb = dt'b softplus'(dt + dt_bias).
-// A thread keeps eight states (pairs in one instruction) of two channels; a
+// A thread keeps eight states (pairs in one instruction) of two channels, or
+// four where shared memory then holds three blocks per SM or there are few; a
 // block works on SCAN_WARPS neighbouring warp tiles of channels and one
 // segment of a line, SCAN_R rows at a time from the end.  The states inside
 // come again from the one kept before those rows: a first run leaves every
@@ -24,15 +25,15 @@ namespace selinv {
 namespace {
 
 constexpr int SCAN_S = 4;       // rows whose states and decays are in registers together
-constexpr int SCAN_P = 2;       // rows whose parts of Bb and Cb are in shared memory together
 
 // lane = nl * LD + dl holds the channels 2 dl, 2 dl + 1 and the states nl * SN on.
 template <class T_, int NP_> struct ScanBwdTile {
     using T = T_;
     using C = typename Elem<T>::C;
     using V = typename Two<C>::V;
-    static constexpr int NP = NP_, SN = (NP == 4 ? 4 : 8) / (sizeof(C) / 4), KP = SN / 2, LN = NP / SN, LD = 32 / LN, CW = 2 * LD;
+    static constexpr int NP = NP_, SN = NP == 4 && sizeof(C) == 8 ? 2 : NP > 16 - (sizeof(T) == 2) && sizeof(C) == 4 ? 8 : 4, KP = SN / 2, LN = NP / SN, LD = 32 / LN, CW = 2 * LD;
     static constexpr int PER = (SCAN_R + LN - 1) / LN;          // rows whose steps and outputs a lane forms
+    static constexpr int P = SN == 4 && sizeof(T) == 2 ? 4 : 2;     // rows whose parts of Bb and Cb are in shared memory together
     static constexpr int Q = 16 / (int)sizeof(C), CHUNKS = 2 * SN / Q;      // 16 bytes of sums; B's states, then C's
 };
 template <class K> struct ScanBwdSmem {
@@ -40,7 +41,7 @@ template <class K> struct ScanBwdSmem {
     using T = typename K::T;
     alignas(16) T x[SCAN_R][K::CW], dt_raw[SCAN_R][K::CW], z[SCAN_R][K::CW], yb_raw[SCAN_R][K::CW];
     alignas(16) C dt[SCAN_R][K::CW], yb[SCAN_R][K::CW], gb[SCAN_R][K::CW], qa[SCAN_R][K::CW], hc[SCAN_R][K::CW];
-    alignas(16) C part[SCAN_P][K::LN][K::CHUNKS][K::LD][K::Q];
+    alignas(16) C part[K::P][K::LN][K::CHUNKS][K::LD][K::Q];
     alignas(16) C bc[SCAN_R][2 * K::NP];
     alignas(16) typename K::V h[SCAN_R / SCAN_S - 1][2 * K::KP][32];    // states before rows SCAN_S, 2 SCAN_S, ...
 };
@@ -195,22 +196,22 @@ template <class K> struct ScanBwd {
                 out[SN + 2 * j] = sc[j].x, out[SN + 2 * j + 1] = sc[j].y;
             }
 #pragma unroll
-            for (int i = 0; i < K::CHUNKS; ++i) put<K::Q>(&sm.part[r % SCAN_P][nl][i][lane % K::LD][0], out + i * K::Q);
+            for (int i = 0; i < K::CHUNKS; ++i) put<K::Q>(&sm.part[r % K::P][nl][i][lane % K::LD][0], out + i * K::Q);
             if (first && o.stateb_out) store(static_cast<C *>(o.stateb_out) + p.rows.number(sequence(k0, st, t), line) * dn, g);
-            if (r % SCAN_P == 0) {
+            if (r % K::P == 0) {
                 __syncwarp();
                 sums(t);
                 __syncwarp();
             }
         }
     }
-    // Bb's and Cb's sums over this warp's channels for rows t .. t + SCAN_P - 1: a pair of states at a time, from another
+    // Bb's and Cb's sums over this warp's channels for rows t .. t + P - 1: a pair of states at a time, from another
     // lane's part on each, so that the lanes read other banks.
     SELINV_DEVINL void sums(int t) const
     {
         constexpr int HALVES = K::Q / 2, PAIRS = K::LN * K::CHUNKS * HALVES;
 #pragma unroll
-        for (int i = lane; i < SCAN_P * PAIRS; i += 32) {
+        for (int i = lane; i < K::P * PAIRS; i += 32) {
             const int r = i / PAIRS, pair = i % PAIRS, half = pair % HALVES, chunk = pair / HALVES;
             const int m = chunk / K::CHUNKS, ch = chunk % K::CHUNKS;
             V v[K::LD];
@@ -227,8 +228,15 @@ template <class K> struct ScanBwd {
     }
 };
 
+// Blocks per SM that shared memory and registers allow; three keep to 168 registers, where eight states would spill (16
+// states: in 16-bit types 963 us with eight and two blocks, 1036 with four and three, 4 x 2048 x 4096; in float 175 and
+// 141, 3 x 517 x 1250).
+template <class K> constexpr int scan_bwd_blocks = K::SN <= 4 && 3 * (sizeof(ScanBwdBlock<K>) + 1024) <= 228 * 1024   ? 3
+                                                   : 2 * (sizeof(ScanBwdBlock<K>) + 1024) <= 228 * 1024 ? 2
+                                                                                                        : 1;
+
 template <class K>
-__global__ void __launch_bounds__(SCAN_WARPS * 32)
+__global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
     scan_backward_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ ScanGrads o)
 {
     using T = typename K::T;

@@ -27,6 +27,10 @@ template <class T> int scan_backward_channels(int n)
 {
     return with_states(n, [](auto np) { return ScanBwdTile<T, np.value>::CW; });
 }
+template <class T> int scan_backward_blocks(int n)
+{
+    return with_states(n, [](auto np) { return scan_bwd_blocks<ScanBwdTile<T, np.value>>; });
+}
 template <class T> cudaError_t scan_launch(const ScanArgs &p, int lanes, cudaStream_t s)
 {
     return with_states(p.n, [&](auto np) {
@@ -58,6 +62,7 @@ template <class T> cudaError_t scan_step_launch(const ScanStepArgs &p, cudaStrea
 
 #define SELINV_SCAN_INSTANCES(T)                                                                   \
     template int scan_backward_channels<T>(int);                                                   \
+    template int scan_backward_blocks<T>(int);                                                     \
     template cudaError_t scan_launch<T>(const ScanArgs &, int, cudaStream_t);                      \
     template cudaError_t scan_backward_launch<T>(const ScanArgs &, const ScanGrads &, cudaStream_t); \
     template cudaError_t scan_step_launch<T>(const ScanStepArgs &, cudaStream_t);

@@ -10,6 +10,7 @@ namespace selinv {
 constexpr int scan_least_lanes(int n) { return n <= 16 ? 1 : n <= 32 ? 2 : 4; }
 constexpr int scan_most_lanes(int n) { return n <= 4 ? 1 : n <= 8 ? 2 : 4; }
 template <class T> int scan_backward_channels(int n);
+template <class T> int scan_backward_blocks(int n);     // resident per SM
 template <class T> cudaError_t scan_launch(const ScanArgs &p, int lanes, cudaStream_t s);
 template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, cudaStream_t s);
 template <class T> cudaError_t scan_step_launch(const ScanStepArgs &p, cudaStream_t s);
