@@ -216,7 +216,7 @@ selinv_status conv_check(const selinv_conv_inputs &a)
 int64_t conv_chunk(const selinv_conv_inputs &a, bool backward)
 {
     const int64_t per = a.dtype == SELINV_F64 ? 2 : 4, vecs = div_up(a.d, per) * (a.lines > 0 ? a.lines : 1);
-    const int64_t want = 1024 * (int64_t)sm_count(), least = backward ? 32 : 16, most = 128;
+    const int64_t want = 1024 * (int64_t)sm_count(), least = 16, most = 128;
     int64_t rows = div_up(a.rows, div_up(want, vecs));
     rows = rows < least ? least : rows > most ? most : rows;
     return div_up(rows, 4) * 4;

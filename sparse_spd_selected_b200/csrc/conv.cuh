@@ -258,9 +258,10 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
             Pack<T, E> xr[U], yr[U];
             bool ahead = false;
             for (int t = r; t - (K - 1) < m1;) {
-                // U rows t .. t + U - 1 of this chunk whose outputs are rows of this sequence that no final state holds
+                // U rows from s on, none of them behind the sequence, no output of theirs a state's
                 const auto plain = [&](int s) {
-                    return whole && s + U <= min(end, w.r1) && s - (K - 1) >= max(start, w.r0) && (!stateb || s + U - K < end - (K - 1));
+                    return whole && s + U <= end && (!stateb || s + U - K < end - (K - 1)) &&
+                           (!stateb_out || s - (K - 1) >= start);
                 };
                 if (plain(t)) {
                     if (!ahead) {
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
                         unpack(xr[i], win[K - 1 + i]);
                         unpack(yr[i], g[i]);
                     }
-                    ahead = plain(t + U);
+                    ahead = t + U - (K - 1) < m1 && plain(t + U);
                     if (ahead) {
                         load_rows(x + (int64_t)(t + U) * p.x.row, p.x.row, p.x.wide, xr);
                         load_rows(yb + (int64_t)(t + U) * p.yb.row, p.yb.row, p.yb.wide, yr);
@@ -289,10 +290,13 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
                     }
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
+                        const bool ours = t + i < w.r1;
+                        const int m = t + i - (K - 1);
                         V v[EP];
 #pragma unroll
                         for (int e = 0; e < EP; ++e) {
                             ring[K - 1 + i][e] = g[i][e];
+                            if (!ours) g[i][e] = none[e];       // summed by the next chunk
                             bsum[e] = add2(bsum[e], g[i][e]);
                             v[e] = mul2(wt[K - 1][e], ring[i][e]);
 #pragma unroll
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
                                 if (j) v[e] = fma2(wt[K - 1 - j][e], ring[i + j][e], v[e]);
                             }
                         }
-                        down_row(xb + (int64_t)(t + i - (K - 1)) * p.xb.row, E, p.xb.wide, v);
+                        if (m >= max(m0, start) && m < m1) down_row(xb + (int64_t)m * p.xb.row, E, p.xb.wide, v);
                     }
                     conv_shift<K, U, EP>(win);
                     conv_shift<K, U, EP>(ring);

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) scan_kernel(const __grid_cons
             T(*out)[CW] = reinterpret_cast<T(*)[CW]>(&sm.dt[0][0]);
             __syncwarp();       // all lanes are done with the steps
 #pragma unroll
-            for (int i = 0; i < PER; ++i) out[nl + LN * i][dl] = Elem<T>::down(v[i]);
+            for (int i = 0; i < PER; i += 2) down2(&out[nl + LN * i][dl], &out[nl + LN * (i + 1)][dl], v[i], v[i + 1]);
             __syncwarp();
             if (p.y.wide && w.nch == CW) {
                 constexpr int LANES = CW / E, ROWS = 32 / LANES;

@@ -70,6 +70,19 @@ template <> struct Elem<__half> {
     SELINV_DEVINL static __half down(float v) { return __float2half_rn(v); }
 };
 
+// Rounds two values to two places: the 16-bit types in one instruction (one value alone takes the special function unit).
+template <class T> SELINV_DEVINL void down2(T *p, T *q, typename Elem<T>::C x, typename Elem<T>::C y)
+{
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w = Elem<T>::pair(x, y);
+        *reinterpret_cast<unsigned short *>(p) = (unsigned short)w;
+        *reinterpret_cast<unsigned short *>(q) = (unsigned short)(w >> 16);
+    } else {
+        *p = Elem<T>::down(x);
+        *q = Elem<T>::down(y);
+    }
+}
+
 // E consecutive elements as they lie in memory, held in 32-bit words.
 template <class T, int E> struct Pack {
     static_assert(E * sizeof(T) % 4 == 0 && E * sizeof(T) <= 16, "4, 8 or 16 bytes");
