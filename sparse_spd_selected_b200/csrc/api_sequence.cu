@@ -122,6 +122,9 @@ Spread scan_spread(const selinv_scan_inputs &a, bool backward)
         if (b * segs < 2 * sms) segs = 2 * sms / b < a.rows / 32 ? 2 * sms / b : a.rows / 32;
         s.segs = (int)(segs < 1 ? 1 : segs < MAX_SEGS ? segs : MAX_SEGS);
     }
+    // the backward's run over the segments' ends: lanes until there are three blocks per SM
+    if (backward)
+        while (s.lanes < scan_most_lanes(n) && blocks(32 / s.lanes) * s.segs < 3 * sms) s.lanes *= 2;
     s.tiles = a.groups * div_up(per, cw);
     s.blocks = a.groups * div_up(div_up(per, cw), SCAN_BLOCK_TILES);
     s.seg_rows = div_up(div_up(a.rows, s.segs), SCAN_KEEP_ROWS) * SCAN_KEEP_ROWS;
@@ -183,6 +186,7 @@ selinv_status scan_args(const selinv_scan_inputs &a, const Spread &s, ScanArgs &
     p.B_group = a.B_group, p.C_group = a.C_group;
     p.A = a.A, p.D = a.D, p.dt_bias = a.dt_bias, p.state = a.state;
     p.segs = s.segs, p.seg_rows = (int)s.seg_rows;
+    p.ends_lanes = s.lanes;
     return SELINV_OK;
 }
 

@@ -19,7 +19,7 @@
 // order.
 #pragma once
 
-#include "scan.cuh"
+#include "scan_forward.cuh"
 
 namespace selinv {
 namespace {
@@ -502,64 +502,65 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
     }
 }
 
-// What each segment hands to the row before it, from nothing behind it, and the sum of its steps: a lane per channel, as
+// What each segment hands to the row before it, from nothing behind it, and the sum of its steps: LN lanes per channel, as
 // in the forward.
-template <class T, int NP> struct ScanEndsSmem {
-    using C = typename Elem<T>::C;
+template <class K> struct ScanEndsSmem {
+    using C = typename K::C;
+    using T = typename K::T;
     struct Raw {
-        alignas(16) T dt[SCAN_R][32], yb[SCAN_R][32], z[SCAN_R][32], c[SCAN_R][NP];
+        alignas(16) T dt[SCAN_R][K::CW], yb[SCAN_R][K::CW], z[SCAN_R][K::CW], c[SCAN_R][K::NP];
     } raw[2];
-    alignas(16) C dt[SCAN_R][32], yb[SCAN_R][32], c[SCAN_R][NP];
+    alignas(16) C dt[SCAN_R][K::CW], yb[SCAN_R][K::CW], c[SCAN_R][K::NP];
 };
-template <class T, int NP>
-SELINV_DEVINL void scan_ends_row(const ScanEndsSmem<T, NP> &sm, int t, int lane, const typename Two<typename Elem<T>::C>::V *A2,
-                                 typename Two<typename Elem<T>::C>::V *g)
+template <class K>
+SELINV_DEVINL void scan_ends_row(const ScanEndsSmem<K> &sm, int t, int dl, int n0, const typename K::V *A2, typename K::V *g)
 {
-    using C = typename Elem<T>::C;
-    using V = typename Two<C>::V;
-    const C dt = sm.dt[t][lane], yb = sm.yb[t][lane];
+    using C = typename K::C;
+    using V = typename K::V;
+    const C dt = sm.dt[t][dl], yb = sm.yb[t][dl];
     const V d2 = make2(dt, dt), y2 = make2(yb, yb);
 #pragma unroll
-    for (int j = 0; j < NP / 2; j += 2) {
+    for (int j = 0; j < K::KP; j += 2) {
         V c[2];
-        get<2>(&sm.c[t][2 * j], c);
+        get<2>(&sm.c[t][n0 + 2 * j], c);
 #pragma unroll
         for (int i = 0; i < 2; ++i) g[j + i] = mul2(decay2(d2, A2[j + i]), fma2(c[i], y2, g[j + i]));
     }
 }
-template <class T, int NP>
+template <class K>
 __global__ void __launch_bounds__(SCAN_WARPS * 32)
     scan_backward_ends_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ ScanGrads o)
 {
-    using C = typename Elem<T>::C;
-    using V = typename Two<C>::V;
-    constexpr int R = SCAN_R;
+    using T = typename K::T;
+    using C = typename K::C;
+    using V = typename K::V;
+    constexpr int R = SCAN_R, LN = K::LN, SN = K::SN, KP = K::KP, CW = K::CW, PER = K::PER;
     extern __shared__ __align__(16) char smem_raw[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    ScanEndsSmem<T, NP> &sm = reinterpret_cast<ScanEndsSmem<T, NP> *>(smem_raw)[warp];
+    ScanEndsSmem<K> &sm = reinterpret_cast<ScanEndsSmem<K> *>(smem_raw)[warp];
     ScanPlace w;
-    if (!scan_place(p, warp, blockDim.x / 32, 32, w) || w.r0 >= w.r1 || w.seg == 0) return;
-    const int n = p.n;
-    const bool in = lane < w.nch;
+    if (!scan_place(p, warp, blockDim.x / 32, CW, w) || w.r0 >= w.r1 || w.seg == 0) return;
+    const int nl = lane / CW, dl = lane % CW, n0 = nl * SN, n = p.n - n0;
+    const bool in = dl < w.nch;
     const T *dt = static_cast<const T *>(p.dt.p) + w.line * p.dt.line + w.c0;
     const T *z = p.z.p ? static_cast<const T *>(p.z.p) + w.line * p.z.line + w.c0 : nullptr;
     const T *Cc = static_cast<const T *>(p.C.p) + w.line * p.C.line + w.group * p.C_group;
     const T *yb = static_cast<const T *>(o.yb.p) + w.line * o.yb.line + w.c0;
-    const int64_t own = (int64_t)(w.c0 + lane) * n, dn = p.d * n;
-    V A2[NP / 2], g[NP / 2];
-    load_states<NP>(static_cast<const C *>(p.A) + own, n, in, A2);
+    const int64_t own = (int64_t)(w.c0 + dl) * p.n + n0, dn = p.d * p.n;
+    V A2[KP], g[KP];
+    load_states<SN>(static_cast<const C *>(p.A) + own, n, in, A2);
 #pragma unroll
-    for (int j = 0; j < NP / 2; ++j) A2[j] = mul2(A2[j], make2(log2e<C>(), log2e<C>()));
-    zero_states<NP>(g);
-    const C bias = in && p.dt_bias ? static_cast<const C *>(p.dt_bias)[w.c0 + lane] : (C)0;
+    for (int j = 0; j < KP; ++j) A2[j] = mul2(A2[j], make2(log2e<C>(), log2e<C>()));
+    zero_states<SN>(g);
+    const C bias = in && p.dt_bias ? static_cast<const C *>(p.dt_bias)[w.c0 + dl] : (C)0;
     C total = 0;
-    const bool full = p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.C.wide && w.nch == 32 && whole_n<T>(n);
+    const bool full = p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.C.wide && w.nch == CW && whole_n<T>(p.n);
     auto fetch_as = [&](auto whole, int r, int to) {
         constexpr bool F = whole.value;
-        raw_fetch<32, F>(sm.raw[to].dt, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
-        raw_fetch<32, F>(sm.raw[to].yb, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
-        if (z) raw_fetch<32, F>(sm.raw[to].z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
-        raw_fetch_n<32, F>(sm.raw[to].c, Cc, p.C.row, r, w.r1, n, p.C.wide, lane);
+        raw_fetch<CW, F>(sm.raw[to].dt, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
+        raw_fetch<CW, F>(sm.raw[to].yb, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
+        if (z) raw_fetch<CW, F>(sm.raw[to].z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
+        raw_fetch_n<32, F>(sm.raw[to].c, Cc, p.C.row, r, w.r1, p.n, p.C.wide, lane);
         cp_async_commit();
     };
     auto fetch = [&](int r, int to) {
@@ -568,8 +569,8 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
         else
             fetch_as(std::false_type(), r, to);
     };
-    raw_clear_n<32>(sm.raw[0].c, n, lane);
-    raw_clear_n<32>(sm.raw[1].c, n, lane);
+    raw_clear_n<32>(sm.raw[0].c, p.n, lane);
+    raw_clear_n<32>(sm.raw[1].c, p.n, lane);
     __syncwarp();
     int k = p.rows.find(w.r1 - 1);          // the sequence of the row at hand
     int rt = w.r0 + (w.r1 - w.r0 - 1) / R * R, now = 0;
@@ -585,28 +586,29 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
         if (rt > w.r0) fetch(rt - R, now ^ 1);
         raw_stage_n<32>(sm.c, raw.c, lane);
         {
-            C a[R], y[R];
+            C a[PER], y[PER];
 #pragma unroll
-            for (int t = 0; t < R; ++t) {
-                a[t] = Elem<T>::up(raw.dt[t][lane]) + bias;
-                y[t] = Elem<T>::up(raw.yb[t][lane]);
+            for (int i = 0; i < PER; ++i) {
+                a[i] = Elem<T>::up(raw.dt[nl + LN * i][dl]) + bias;
+                y[i] = Elem<T>::up(raw.yb[nl + LN * i][dl]);
             }
             if (p.softplus) {
 #pragma unroll
-                for (int t = 0; t < R; ++t) a[t] = softplus_(a[t]);
+                for (int i = 0; i < PER; ++i) a[i] = softplus_(a[i]);
             }
             if (z) {
 #pragma unroll
-                for (int t = 0; t < R; ++t) {
-                    const C v = Elem<T>::up(raw.z[t][lane]);
-                    y[t] *= v * sigmoid_(v);
+                for (int i = 0; i < PER; ++i) {
+                    const C v = Elem<T>::up(raw.z[nl + LN * i][dl]);
+                    y[i] *= v * sigmoid_(v);
                 }
             }
 #pragma unroll
-            for (int t = 0; t < R; ++t) {
-                sm.dt[t][lane] = a[t];
-                sm.yb[t][lane] = y[t];
-                if (t < nr) total += a[t];
+            for (int i = 0; i < PER; ++i) {
+                const int t = nl + LN * i;
+                sm.dt[t][dl] = a[i];
+                sm.yb[t][dl] = y[i];
+                if (t < nr) total += a[i];
             }
         }
         __syncwarp();
@@ -614,26 +616,41 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
             if ((st >> (t + 1)) & 1u) {         // the last row of its sequence
                 if (rt + t < p.rows.start(k)) --k;
                 if (o.stateb)
-                    load_states<NP>(static_cast<const C *>(o.stateb) + p.rows.number(k, w.line) * dn + own, n, in, g);
+                    load_states<SN>(static_cast<const C *>(o.stateb) + p.rows.number(k, w.line) * dn + own, n, in, g);
                 else
-                    zero_states<NP>(g);
+                    zero_states<SN>(g);
             }
             // down to the row behind the next such row
             const uint32_t earlier = st & ((2u << t) - 2u);
             const int te = earlier ? 31 - __clz(earlier) : 0;
             for (; t - 3 >= te; t -= 4) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) scan_ends_row<T, NP>(sm, t - i, lane, A2, g);
+                for (int i = 0; i < 4; ++i) scan_ends_row(sm, t - i, dl, n0, A2, g);
             }
-            for (; t >= te; --t) scan_ends_row<T, NP>(sm, t, lane, A2, g);
+            for (; t >= te; --t) scan_ends_row(sm, t, dl, n0, A2, g);
         }
         __syncwarp();
     }
+#pragma unroll
+    for (int m = CW; m < 32; m *= 2) total += shfl_xor_(total, m);
     if (in) {
         const int64_t piece = w.line * p.segs + w.seg;
-        store_states<NP>(static_cast<C *>(p.ends) + piece * dn + own, n, in, g);
-        static_cast<C *>(p.sums)[piece * p.d + w.c0 + lane] = total;
+        store_states<SN>(static_cast<C *>(p.ends) + piece * dn + own, n, in, g);
+        if (nl == 0) static_cast<C *>(p.sums)[piece * p.d + w.c0 + dl] = total;
     }
+}
+template <class K> cudaError_t scan_ends_run(const ScanArgs &p, const ScanGrads &o, cudaStream_t s)
+{
+    constexpr int warps = SCAN_WARPS * sizeof(ScanEndsSmem<K>) <= 227 * 1024 ? SCAN_WARPS : SCAN_WARPS / 2;
+    constexpr int bytes = warps * (int)sizeof(ScanEndsSmem<K>);
+    static_assert(bytes <= 227 * 1024, "fits an SM");
+    const int64_t tiles = (p.d / p.groups + K::CW - 1) / K::CW;
+    const dim3 grid((unsigned)(p.lines * p.segs), (unsigned)(p.groups * ((tiles + warps - 1) / warps)));
+    const cudaError_t e =
+        cudaFuncSetAttribute(scan_backward_ends_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    scan_backward_ends_kernel<K><<<grid, warps * 32, bytes, s>>>(p, o);
+    return cudaSuccess;
 }
 
 // Bb and Cb from the blocks' sums, and Ab, Db, dt_biasb from the segments': the first `bc_blocks` blocks take one
@@ -695,14 +712,8 @@ template <class T, int NP> cudaError_t scan_backward_run(const ScanArgs &p, cons
     constexpr int bytes = (int)sizeof(ScanBwdBlock<K>);
     static_assert(bytes <= 227 * 1024, "fits an SM");
     if (p.segs > 1) {
-        constexpr int warps = SCAN_WARPS * sizeof(ScanEndsSmem<T, NP>) <= 227 * 1024 ? SCAN_WARPS : SCAN_WARPS / 2;
-        constexpr int ends = warps * (int)sizeof(ScanEndsSmem<T, NP>);
-        const int64_t t32 = (per + 31) / 32;
-        const dim3 g((unsigned)(p.lines * p.segs), (unsigned)(p.groups * ((t32 + warps - 1) / warps)));
-        cudaError_t e =
-            cudaFuncSetAttribute(scan_backward_ends_kernel<T, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, ends);
+        const cudaError_t e = with_lanes<T, NP>(p.ends_lanes, [&](auto k) { return scan_ends_run<decltype(k)>(p, o, s); });
         if (e != cudaSuccess) return e;
-        scan_backward_ends_kernel<T, NP><<<g, warps * 32, ends, s>>>(p, o);
     }
     cudaError_t e = cudaFuncSetAttribute(scan_backward_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;

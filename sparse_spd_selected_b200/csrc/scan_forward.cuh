@@ -264,5 +264,20 @@ template <class K> cudaError_t scan_run(const ScanArgs &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
+// Calls f with the tile of NP states and so many lanes per channel.
+template <class T, int NP, class F> cudaError_t with_lanes(int lanes, F f)
+{
+    if constexpr (NP <= 16) {
+        if (lanes == 1) return f(ScanFwdTile<T, NP, 1>());
+    }
+    if constexpr (NP == 8 || NP == 16 || NP == 32) {
+        if (lanes == 2) return f(ScanFwdTile<T, NP, 2>());
+    }
+    if constexpr (NP >= 16) {
+        if (lanes == 4) return f(ScanFwdTile<T, NP, 4>());
+    }
+    return cudaErrorInvalidValue;
+}
+
 }  // namespace
 }  // namespace selinv

@@ -34,17 +34,7 @@ template <class T> int scan_backward_blocks(int n)
 template <class T> cudaError_t scan_launch(const ScanArgs &p, int lanes, cudaStream_t s)
 {
     return with_states(p.n, [&](auto np) {
-        constexpr int NP = np.value;
-        if constexpr (NP <= 16) {
-            if (lanes == 1) return scan_run<ScanFwdTile<T, NP, 1>>(p, s);
-        }
-        if constexpr (NP == 8 || NP == 16 || NP == 32) {
-            if (lanes == 2) return scan_run<ScanFwdTile<T, NP, 2>>(p, s);
-        }
-        if constexpr (NP >= 16) {
-            if (lanes == 4) return scan_run<ScanFwdTile<T, NP, 4>>(p, s);
-        }
-        return cudaErrorInvalidValue;
+        return with_lanes<T, np.value>(lanes, [&](auto k) { return scan_run<decltype(k)>(p, s); });
     });
 }
 template <class T> cudaError_t scan_backward_launch(const ScanArgs &p, const ScanGrads &o, cudaStream_t s)

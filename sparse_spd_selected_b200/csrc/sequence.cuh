@@ -408,6 +408,7 @@ struct ScanArgs {
     void *state_out, *kept;     // may be null
     // lines cut into segments of seg_rows rows: the state each leaves behind from zero, and the sum of its steps
     int segs, seg_rows;
+    int ends_lanes;             // lanes per channel of the backward's run over the segments' ends
     void *ends, *sums;
 };
 
