@@ -1225,6 +1225,14 @@ def causal_conv_backward(x, weight, yb, *, bias=None, stateb=None, silu=False, s
     return {"xb": xb, "weightb": weightb, "biasb": biasb, "stateb": new}
 
 
+def _not_captured(what, *inputs):
+    """Refuses a differentiable call in a stream capture: its backward pass would hand gradients to leaves whose
+    accumulators may belong to another stream, that of an eager graph, which a capture cannot join."""
+    if torch.is_grad_enabled() and torch.cuda.is_current_stream_capturing() and \
+            any(t is not None and t.requires_grad for t in inputs):
+        raise ValueError(f"{what} cannot be captured: capture the forward and the backward call instead")
+
+
 class _CausalConvFn(torch.autograd.Function):
     """y, state = causal_conv(...) with its analytic backward."""
 
@@ -1239,6 +1247,8 @@ class _CausalConvFn(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, yb, stateb):
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("causal_conv_ad's backward cannot be captured: capture causal_conv_backward instead")
         x, weight, bias, state = ctx.saved_tensors
         yb = torch.zeros_like(x, memory_format=torch.contiguous_format) if yb is None else _view_or_copy(yb)
         r = causal_conv_backward(x, weight, yb, bias=bias, stateb=None if stateb is None else stateb.contiguous(),
@@ -1258,7 +1268,8 @@ def _view_or_copy(t):
 
 def causal_conv_ad(x, weight, bias=None, *, silu=False, state=None, plan=None):
     """Differentiable causal_conv: returns (y, state); gradients reach x, weight, bias and state through
-    causal_conv_backward."""
+    causal_conv_backward.  Refused in a stream capture, where causal_conv and causal_conv_backward are called."""
+    _not_captured("causal_conv_ad", x, weight, bias, state)
     return _CausalConvFn.apply(x, weight, bias, state, silu, plan)
 
 
@@ -1431,6 +1442,8 @@ class _SelectiveScanFn(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, yb, stateb):
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("selective_scan_ad's backward cannot be captured: capture selective_scan_backward instead")
         x, dt, A, B, C, D, z, dt_bias, state, kept = ctx.saved_tensors
         yb = torch.zeros_like(x, memory_format=torch.contiguous_format) if yb is None else _view_or_copy(yb)
         r = selective_scan_backward(kept, x, dt, A, B, C, yb, D=D, stateb=None if stateb is None else stateb.contiguous(),
@@ -1440,7 +1453,8 @@ class _SelectiveScanFn(torch.autograd.Function):
 
 def selective_scan_ad(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=False, state=None, plan=None):
     """Differentiable selective_scan: returns (y, state); gradients reach every tensor through
-    selective_scan_backward."""
+    selective_scan_backward.  Refused in a stream capture, where selective_scan and selective_scan_backward are called."""
+    _not_captured("selective_scan_ad", x, dt, A, B, C, D, z, dt_bias, state)
     return _SelectiveScanFn.apply(x, dt, A, B, C, D, z, dt_bias, state, softplus, plan)
 
 

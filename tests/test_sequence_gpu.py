@@ -668,3 +668,79 @@ def test_refusals(cuda_ok):
     whole = torch.zeros(5, 3, 8, device="cuda")
     with pytest.raises(ValueError):
         selinv.causal_conv_step(whole[:3], x[:2], w, cache_out=whole[1:4])
+
+
+def test_differentiable_calls_are_refused_in_a_capture(cuda_ok):
+    """While an eager graph of the same leaves lives, too; the leaves and the eager graph are usable afterwards."""
+    v, yb, _ = scan_inputs(18, torch.float32, (1, 9), 8, 4, 1)
+    x = v["x"].clone().requires_grad_(True)
+    w = torch.ones(8, 4, device="cuda", requires_grad=True)
+    call = lambda: selinv.selective_scan_ad(x, v["dt"], v["A"], v["B"], v["C"])[0]     # noqa: E731
+    y = call()
+    c, _ = selinv.causal_conv_ad(x, w)
+    torch.cuda.synchronize()
+    for bad in (call, lambda: selinv.causal_conv_ad(x, w)):
+        g = torch.cuda.CUDAGraph()
+        with pytest.raises(ValueError):
+            with torch.cuda.graph(g):
+                bad()
+    g = torch.cuda.CUDAGraph()
+    with torch.no_grad(), torch.cuda.graph(g):
+        z = call()
+    g.replay()
+    (y.sum() + c.sum()).backward()
+    torch.cuda.synchronize()
+    assert torch.equal(z, y.detach()) and bool(torch.isfinite(x.grad).all()) and bool(torch.isfinite(w.grad).all())
+
+
+def test_two_streams_at_once(cuda_ok):
+    """Calls in flight together, of shapes that are cut differently, give what they give alone."""
+    cases = [scan_inputs(20 + i, torch.float32, (2, rows), d, 16, 1)[:2] for i, (rows, d) in enumerate(((500, 40), (300, 900)))]
+
+    def run(v, yb):
+        args = (v["x"], v["dt"], v["A"], v["B"], v["C"])
+        r = selinv.selective_scan(*args, v["D"], z=v["z"], keep=True)
+        b = selinv.selective_scan_backward(r["kept"], *args, yb, D=v["D"], z=v["z"])
+        return [r["y"], r["state"], b["xb"], b["Ab"], b["Bb"], b["Cb"]]
+
+    want = [run(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(5):
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append(run(*c))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
+
+
+def test_workspace_is_the_callers(cuda_ok):
+    """A workspace of the right size serves call after call; a smaller one is refused."""
+    v, yb, _ = scan_inputs(22, torch.float32, (1, 600), 16, 16, 1)
+    args = (v["x"], v["dt"], v["A"], v["B"], v["C"])
+    want = selinv.selective_scan(*args, keep=True)
+    ws = torch.full((1 << 24,), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        got = selinv.selective_scan(*args, keep=True, workspace=ws)
+        b = selinv.selective_scan_backward(got["kept"], *args, yb, workspace=ws)
+    assert torch.equal(got["y"], want["y"]) and bool(torch.isfinite(b["Ab"]).all())
+    with pytest.raises(ValueError):
+        selinv.selective_scan(*args, workspace=ws[:16])
+    with pytest.raises(ValueError):
+        selinv.selective_scan_backward(got["kept"], *args, yb, workspace=ws[:16])
+
+
+def test_against_the_selected_inverse(cuda_ok):
+    """Two rows of the scan are the solve of a block lower-bidiagonal system: the blocks that bidiag returns give them."""
+    v, _, _ = scan_inputs(23, torch.float64, (1, 2), 3, 4, 1, gate=False, skip=False)
+    step = torch.nn.functional.softplus(v["dt"][0] + v["dt_bias"])
+    decay = torch.exp(step[1][:, None] * v["A"])
+    eye = torch.eye(4, dtype=torch.float64, device="cuda").expand(3, 2, 4, 4).contiguous()
+    lower = -torch.diag_embed(decay)[:, None].contiguous()
+    g = selinv.bidiag(eye, lower)
+    u = (step * v["x"][0])[:, :, None] * v["B"][0]                  # [row, channel, state]
+    h1 = (g["G_lower"][:, 0] @ u[0][..., None] + g["G_diag"][:, 1] @ u[1][..., None])[..., 0]
+    r = selinv.selective_scan(v["x"], v["dt"], v["A"], v["B"], v["C"], dt_bias=v["dt_bias"], softplus=True)
+    assert torch.allclose(r["state"][0], h1, rtol=1e-13, atol=1e-14)
