@@ -495,7 +495,10 @@ selinv_status selinv_tree_backward(const selinv_tree_plan_t *plan, selinv_dtype 
  *   - Arrays [lines, rows, d] come as a selinv_view: channels are contiguous,
  *     the strides between rows and lines are the caller's (in elements, not
  *     negative; inputs may overlap or repeat, outputs may not).  16-byte
- *     alignment of base and strides enables the vectorised paths.
+ *     alignment of base and strides enables the vectorised paths.  A stride
+ *     between rows is below 2^31 (SELINV_ERR_INVALID_ARG beyond), a line has
+ *     at most 2^31 - 65 rows; SELINV_ERR_UNSUPPORTED for more, and for more
+ *     lines x segments or groups x channel tiles than a grid holds.
  *   - Without a table each line is one sequence of `rows` rows.  With a table
  *     there is one line, holding the sequences one after another: `table`
  *     (device, int64, 1 + live + sequences entries) has the first rows of the

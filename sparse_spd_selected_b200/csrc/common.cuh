@@ -18,12 +18,6 @@ SELINV_DEVINL void cp_async16(void *smem, const void *gmem)
     unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(smem));
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(gmem) : "memory");
 }
-// 8-byte asynchronous global->shared copy (through L1).
-SELINV_DEVINL void cp_async8(void *smem, const void *gmem)
-{
-    unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(smem));
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(s), "l"(gmem) : "memory");
-}
 // L2 eviction policies (createpolicy) for cache-hinted copies and stores:
 // data streamed once leaves L2 first, so lines that are read back soon (the
 // workspace slots between the two sweeps) stay resident.

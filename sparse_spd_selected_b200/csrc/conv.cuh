@@ -8,7 +8,10 @@
 // in one instruction) and runs down a chunk of rows with the last K - 1 inputs
 // in registers, four rows at a time with the next four on their way, so that
 // neighbouring threads read whole lines and each row is fetched once, but for
-// the K - 1 rows before a chunk.
+// the K - 1 rows before a chunk.  8 x 2048 x 4096, K = 4, bfloat16 with silu: 70
+// us for 268 MB (0.58 of a plain copy's rate; the silu's power of two and
+// reciprocal keep the special function unit half busy), the backward 137 us for
+// 403 MB (0.45; it forms the output again).
 #pragma once
 
 #include "sequence.cuh"

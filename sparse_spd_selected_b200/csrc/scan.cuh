@@ -21,6 +21,13 @@ struct ScanPlace {
     int r0, r1, seg, group, c0, nch;     // c0: first channel (of all d); nch <= CW of them
 };
 
+// 8-byte asynchronous copy from global to shared memory.
+SELINV_DEVINL void cp_async8(void *smem, const void *gmem)
+{
+    const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(smem));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(s), "l"(gmem) : "memory");
+}
+
 // Small vectors in shared memory.
 template <int N> SELINV_DEVINL void put(float *p, const float *v)
 {
@@ -118,7 +125,7 @@ SELINV_DEVINL void raw_fetch(T (*to)[CW], const T *from, int stride, int r, int 
     }
 }
 // The next such tile into L2.
-template <int CW, class T>
+template <class T>
 SELINV_DEVINL void raw_prefetch(const T *from, int stride, int r, int r1, int nch, int lane)
 {
     if (lane < SCAN_R && r + lane < r1 && nch > 0) prefetch_l2(from + (int64_t)(r + lane) * stride);
@@ -209,7 +216,9 @@ template <int N, class V> SELINV_DEVINL void zero_states(V *v)
 }
 
 // What the segments s, s + by, ... before `to` hand on to N states of one channel (own: their place in a [d, n] array):
-// the first one's own, decayed by each later one's sum of steps and joined to that one's own.
+// the first one's own, decayed by each later one's sum of steps and joined to that one's own.  The decays of a whole
+// segment are taken in two halves of at most 2^127 (2^1023) each: steps that let a state grow (dt' A > 0) may leave
+// that range although the state does not, and nothing times that is nothing.
 template <int N, class C>
 SELINV_DEVINL void scan_join(const ScanArgs &p, int64_t line, int s, int to, int by, int64_t channel, int64_t own, int m, bool in,
                              const typename Two<C>::V *A2, typename Two<C>::V *h)
@@ -222,13 +231,16 @@ SELINV_DEVINL void scan_join(const ScanArgs &p, int64_t line, int s, int to, int
     for (s += by; s != to; s += by) {
         V e[N / 2];
         load_states<N>(ends + s * dn, m, in, e);
-        const C t = in ? sums[s * p.d] : (C)0;
+        const C t = in ? sums[s * p.d] / 2 : (C)0, most = sizeof(C) == 4 ? 127 : 1023;
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) h[j] = fma2(decay2(make2(t, t), A2[j]), h[j], e[j]);
+        for (int j = 0; j < N / 2; ++j) {
+            const V a = exp2_2(make2(fmin(t * A2[j].x, most), fmin(t * A2[j].y, most)));
+            h[j] = fma2(a, mul2(a, h[j]), e[j]);
+        }
     }
 }
 
-// warps of a block and channels of a warp.
+// Where this warp works, given a block's warps and a warp's channels; false: no channels are left for it.
 SELINV_DEVINL bool scan_place(const ScanArgs &p, int warp, int warps, int cw, ScanPlace &w)
 {
     const int per = (int)(p.d / p.groups), tiles = (per + cw - 1) / cw;

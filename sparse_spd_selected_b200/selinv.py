@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import struct
 from typing import Optional
@@ -1029,11 +1030,11 @@ def _view(name, t, inner, output=False):
         return t.data_ptr(), 0, 0
     if st[-1] != 1 and sh[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    line = 0
+    line = None
     for i in range(at - 1, -1, -1):
         if sh[i] == 1:
             continue
-        if line == 0:
+        if line is None:
             line, size = st[i], sh[i]
         elif st[i] == line * size:
             size *= sh[i]
@@ -1045,7 +1046,7 @@ def _view(name, t, inner, output=False):
             if stride < need:
                 raise ValueError(f"{name} must not overlap itself")
             need = size * stride
-    return t.data_ptr(), line, st[at]
+    return t.data_ptr(), line or 0, st[at]
 
 
 def _span(t):
@@ -1056,8 +1057,20 @@ def _span(t):
     return t.data_ptr(), t.data_ptr() + n * t.element_size()
 
 
+def _pieces(t):
+    """Elements of a tensor's contiguous pieces, and the distance that all its pieces are multiples of apart (0: one
+    piece)."""
+    width, rest = 1, []
+    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1), key=lambda e: e[1]):
+        if not rest and stride == width:
+            width *= size
+        else:
+            rest.append(stride)
+    return width, math.gcd(*rest)
+
+
 def _apart(name, t, others):
-    """Refuses an output that shares memory with an input.  Two slices of the channels of one array (equal strides)
+    """Refuses an output that shares memory with an input or with another output.  Slices of the channels of one array
     are told apart; anything else that may overlap is refused."""
     a0, a1 = _span(t)
     for other, u in others:
@@ -1066,14 +1079,12 @@ def _apart(name, t, others):
         b0, b1 = _span(u)
         if a1 <= b0 or b1 <= a0:
             continue
-        if t.dtype == u.dtype and t.dim() == u.dim() and t.dim() > 1 and t.stride() == u.stride() and t.stride(-1) == 1:
-            row = min(s for s, n in zip(t.stride()[:-1], t.shape[:-1]) if n > 1) if t.numel() > t.shape[-1] else 0
-            gap = abs(a0 - b0) // t.element_size()
-            if row:
-                gap %= row
-                lo, hi = (t, u) if (a0 < b0) else (u, t)
-                if lo.shape[-1] <= gap and gap + hi.shape[-1] <= row:
-                    continue
+        if t.dtype == u.dtype:
+            (n, row), (m, other_row) = _pieces(t), _pieces(u)
+            row = math.gcd(row, other_row)
+            gap = (b0 - a0) // t.element_size()
+            if row and n <= gap % row and gap % row + m <= row:
+                continue
         raise ValueError(f"{name} must not overlap {other}")
 
 
@@ -1101,8 +1112,9 @@ def _raw_stream(device) -> int:
 
 class SequencePlan:
     """Sequences of the given lengths (0 and more) one after another in one array of rows; the table that the kernels
-    read is cached on the device.  A call may pass arrays with more rows than the plan's: those behind the last
-    sequence are neither read nor written (zero in outputs that the call allocates)."""
+    read is cached on the device and has to live until the calls that read it are done (a captured graph's replays
+    too).  A call may pass arrays with more rows than the plan's: those behind the last sequence are neither read nor
+    written (zero in outputs that the call allocates)."""
 
     def __init__(self, lengths, device=None):
         lengths = [int(n) for n in lengths]
@@ -1144,7 +1156,8 @@ def _rows_of(name, x, plan, inner=1):
 
 
 def _output(out, key, shape, dtype, device, plan, inputs):
-    """out[key], checked, or a new tensor; rows behind a plan's are zero in a new one and left alone in a given one."""
+    """out[key], checked (and added to what later outputs must not overlap), or a new tensor; rows behind a plan's are
+    zero in a new one and left alone in a given one."""
     t = out.get(key) if out else None
     if t is None:
         t = torch.empty(shape, dtype=dtype, device=device)
@@ -1153,6 +1166,7 @@ def _output(out, key, shape, dtype, device, plan, inputs):
         return t
     _like(f"out[{key!r}]", t, dtype, device, shape, contiguous=False)
     _apart(f"out[{key!r}]", t, inputs)
+    inputs.append((f"out[{key!r}]", t))
     return t
 
 
@@ -1162,6 +1176,7 @@ def _dense_output(out, key, shape, dtype, device, inputs):
         return torch.empty(shape, dtype=dtype, device=device)
     _like(f"out[{key!r}]", t, dtype, device, shape)
     _apart(f"out[{key!r}]", t, inputs)
+    inputs.append((f"out[{key!r}]", t))
     return t
 
 
@@ -1190,9 +1205,9 @@ def causal_conv(x, weight, bias=None, *, silu=False, state=None, plan=None, want
     the first row, zero when None.  Returns a dict with y and, if want_state,
     state: the last k-1 inputs of each sequence, from which the next call or
     causal_conv_step goes on.  ``out`` may hold preallocated y and state (not
-    overlapping the inputs)."""
+    overlapping the inputs or each other)."""
     packed, states, d, k = _conv_inputs(x, weight, bias, silu, state, plan)
-    given = (("x", x), ("weight", weight), ("bias", bias), ("state", state)) if out else ()
+    given = [("x", x), ("weight", weight), ("bias", bias), ("state", state)] if out else []
     y = _output(out, "y", x.shape, x.dtype, x.device, plan, given)
     new = _dense_output(out, "state", states, x.dtype, x.device, given) if want_state else None
     _check(lib().selinv_causal_conv(packed, _VIEW.pack(*_view("y", y, 1, out is not None)),
@@ -1209,7 +1224,7 @@ def causal_conv_backward(x, weight, yb, *, bias=None, stateb=None, silu=False, s
     packed, states, d, k = _conv_inputs(x, weight, bias, silu, state, plan)
     dt, dev, ct = x.dtype, x.device, _arith(x.dtype)
     _like("yb", yb, dt, dev, x.shape, contiguous=False)
-    given = (("x", x), ("weight", weight), ("bias", bias), ("state", state), ("yb", yb), ("stateb", stateb)) if out else ()
+    given = [("x", x), ("weight", weight), ("bias", bias), ("state", state), ("yb", yb), ("stateb", stateb)] if out else []
     xb = _output(out, "xb", x.shape, dt, dev, plan, given)
     weightb = _dense_output(out, "weightb", (d, k), ct, dev, given)
     biasb = _dense_output(out, "biasb", (d,), ct, dev, given)
@@ -1316,7 +1331,7 @@ def causal_conv_step(cache, x, weight, bias=None, *, silu=False, index=None, cac
     (batch, d), k = x.shape, weight.shape[1]
     slots, new, at, info = _step_slots(cache, (k - 1, d), batch, index, cache_out, check, dev)
     if out:
-        given = (("x", x), ("weight", weight), ("bias", bias), ("cache", cache), ("cache_out", new))
+        given = [("x", x), ("weight", weight), ("bias", bias), ("cache", cache), ("cache_out", new)]
         y = _output(out, "y", (batch, d), dt, dev, None, given)
         yp, _, y_row = _view("y", y, 1, True)
     else:
@@ -1359,8 +1374,8 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, state, plan):
 
 
 def _scan_given(x, dt, A, B, C, D, z, dt_bias, state, *more):
-    return (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("z", z), ("dt_bias", dt_bias),
-            ("state", state)) + more
+    return [("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("z", z), ("dt_bias", dt_bias),
+            ("state", state), *more]
 
 
 @_placed("x")
@@ -1379,10 +1394,11 @@ def selective_scan(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=Fal
     [rows, d], the sequences one after another, and state [sequences, d, n].
     Returns a dict with y, state (the final states, if want_state) and kept
     (what selective_scan_backward needs, if keep).  ``out`` may hold
-    preallocated y and state (not overlapping the inputs)."""
+    preallocated y and state (not overlapping the inputs or
+    each other)."""
     packed, states, d, n, groups, _ = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, state, plan)
     dev, ct = x.device, _arith(x.dtype)
-    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state) if out else ()
+    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state) if out else []
     y = _output(out, "y", x.shape, x.dtype, dev, plan, given)
     new = _dense_output(out, "state", states, ct, dev, given) if want_state else None
     L = lib()
@@ -1408,7 +1424,7 @@ def selective_scan_backward(kept, x, dt, A, B, C, yb, *, D=None, stateb=None, z=
     L = lib()
     _like("kept", kept, ct, dev, (L.selinv_selective_scan_kept_size(packed) // ct.itemsize,))
     _like("yb", yb, ty, dev, x.shape, False)
-    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state, ("kept", kept), ("yb", yb), ("stateb", stateb)) if out else ()
+    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state, ("kept", kept), ("yb", yb), ("stateb", stateb)) if out else []
     new = {k: _output(out, k, s, ty, dev, plan, given) for k, s in (("xb", x.shape), ("dtb", x.shape), ("Bb", bc), ("Cb", bc))}
     new["zb"] = _output(out, "zb", x.shape, ty, dev, plan, given) if z is not None else None
     for key, ref, shape in (("Ab", A, (d, n)), ("Db", D, (d,)), ("dt_biasb", dt_bias, (d,)), ("stateb", state, states)):

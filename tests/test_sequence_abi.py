@@ -172,6 +172,30 @@ def test_views_and_plans_on_the_host():
             selinv._apart("y", a[:, :4], (("x", other),))
 
 
+def test_repeated_leading_dimensions_are_refused():
+    """A stride of 0 within the leading dimensions does not make one even stride with those outside it."""
+    t = torch.zeros(4, 1, 5, 7)
+    with pytest.raises(ValueError):
+        selinv._view("t", t.expand(4, 3, 5, 7), 1)
+    with pytest.raises(ValueError):
+        selinv._view("t", t[:, 0].expand(3, 4, 5, 7), 1)
+    assert selinv._view("t", t[:1].expand(4, 1, 5, 7), 1)[1:] == (0, 7)
+    assert selinv._view("t", t[:1].expand(4, 3, 5, 7), 1)[1:] == (0, 7)
+    assert selinv._view_or_copy(t.expand(4, 3, 5, 7)).is_contiguous()
+
+
+def test_slices_of_one_array_are_told_apart():
+    a = torch.zeros(6, 40)
+    x, b, c = a[:, :16], a[:, 16:28].view(6, 2, 6), a[:, 28:].view(6, 2, 6)
+    for name, t, others in (("b", b, (x, c)), ("c", c, (x, b)), ("x", x, (b, c)), ("x", x[1:4], (b[2:], x[4:]))):
+        selinv._apart(name, t, [("u", u) for u in others])
+    for t, u in ((b, a[:, 20:30].view(6, 2, 5)), (b, b[:, :1].expand(6, 2, 6)), (x, x), (x, a), (a.view(-1)[10:20], x),
+                 (x, a.view(-1)[10:20]), (x, a[:, :1].expand(6, 16)), (x, a.view(torch.int32)[:, 16:])):
+        with pytest.raises(ValueError):
+            selinv._apart("t", t, [("u", u)])
+    selinv._apart("x", x, [("u", a.view(-1)[17:39])])         # one piece inside a row's gap
+
+
 def test_structures_match_the_header():
     """The packed structures have the header's sizes: every field is 8 bytes."""
     import os

@@ -141,6 +141,36 @@ def test_scan_segments(cuda_ok, kind, rows, d, n):
     check_scan(300 + rows, kind, [rows] * 2, d, n, with_state=True)
 
 
+@pytest.mark.parametrize("kind", ["f32", "f64"])
+def test_scan_growth_beyond_a_segments_range(cuda_ok, kind):
+    """Steps below zero let states grow, over the 32 rows of one segment by more than the type's range: nothing stays
+    nothing, and a small state a finite one."""
+    t, rows, d, n = TYPES[kind], 512, 6, 4
+    step, small = (3.0, 1e-30) if kind == "f32" else (23.0, 1e-250)
+    v, yb, stateb = scan_inputs(78, t, (1, rows), d, n, 1, softplus=False, bias=False, skip=False, states=(1,))
+    v["x"].zero_()
+    v["A"].fill_(-1)
+    v["dt"].zero_()
+    v["dt"][:, 64:96] = -step
+    v["state"].fill_(small)
+    v["state"][:, ::2] = 0
+    yb.zero_()
+    yb[:, -1] = small
+    stateb.zero_()
+    args = (v["x"], v["dt"], v["A"], v["B"], v["C"])
+    r = selinv.selective_scan(*args, z=v["z"], state=v["state"], keep=True)
+    b = selinv.selective_scan_backward(r["kept"], *args, yb, z=v["z"], state=v["state"], stateb=stateb)
+    # the decays' arguments come to 32 steps: an error of a unit each is that many units of the state
+    u = unit(arith(t))
+    bound = plain.scan_bound(rows, n, d, u) + 8 * 32 * step * u
+    flat = {k: a[0] if k in ROWWISE and a is not None else a for k, a in v.items()}
+    ref, mag = (scan_plain(flat, yb[0], stateb, [rows], False, m) for m in (False, True))
+    assert np.isfinite(host(r["y"])).all() and not host(r["state"])[:, ::2].any()
+    near("y", r["y"][0], ref["y"], mag["y"], bound)
+    near("state", r["state"], ref["state"], mag["state"], bound)
+    near("stateb", b["stateb"], ref["stateb"], mag["stateb"], bound)
+
+
 @pytest.mark.parametrize("options", [dict(gate=False), dict(skip=False), dict(bias=False), dict(softplus=False),
                                      dict(gate=False, skip=False, bias=False, softplus=False)])
 def test_scan_without_options(cuda_ok, options):
@@ -465,6 +495,25 @@ def test_gradients_of_expanded_and_repeated_inputs(cuda_ok):
     assert torch.allclose(row.grad, dt2.grad.sum(1, keepdim=True), rtol=1e-13)
 
 
+@pytest.mark.parametrize("scan", [False, True])
+@pytest.mark.parametrize("dims", [(0,), (1,), (0, 1)])
+def test_gradients_of_sums_over_leading_dimensions(cuda_ok, dims, scan):
+    """The cotangent of y then repeats along some of the leading dimensions."""
+    v, _, _ = scan_inputs(991, torch.float64, (2, 3, 6), 4, 3, 1)
+    w = torch.randn(4, 3, dtype=torch.float64, device="cuda")
+    grads = []
+    for dense in (False, True):
+        x = v["x"].clone().requires_grad_(True)
+        u, _ = selinv.causal_conv_ad(x, w, silu=True)
+        y = selinv.selective_scan_ad(v["x"], u, v["A"], v["B"], v["C"], z=v["z"], softplus=True)[0] if scan else u
+        if dense:
+            y.backward((2 * y.detach().sum(dims, keepdim=True)).expand(y.shape).contiguous())
+        else:
+            (y.sum(dims) ** 2).sum().backward()
+        grads.append(x.grad)
+    assert torch.allclose(grads[0], grads[1], rtol=1e-12, atol=1e-14)
+
+
 # ---- strides, streams, graphs -------------------------------------------------
 
 
@@ -744,3 +793,47 @@ def test_against_the_selected_inverse(cuda_ok):
     h1 = (g["G_lower"][:, 0] @ u[0][..., None] + g["G_diag"][:, 1] @ u[1][..., None])[..., 0]
     r = selinv.selective_scan(v["x"], v["dt"], v["A"], v["B"], v["C"], dt_bias=v["dt_bias"], softplus=True)
     assert torch.allclose(r["state"][0], h1, rtol=1e-13, atol=1e-14)
+
+
+def test_outputs_that_overlap_each_other_are_refused(cuda_ok):
+    v, yb, _ = scan_inputs(18, torch.float32, (2, 6), 8, 4, 2, states=(2,))
+    args = (v["x"], v["dt"], v["A"], v["B"], v["C"])
+    kept = selinv.selective_scan(*args, keep=True)["kept"]
+    one, bc = torch.empty_like(v["x"]), torch.empty_like(v["B"])
+    for out in ({"xb": one, "dtb": one}, {"Bb": bc, "Cb": bc}, {"xb": one, "Bb": one.view(2, 6, 2, 4)}):
+        with pytest.raises(ValueError):
+            selinv.selective_scan_backward(kept, *args, yb, out=out)
+    state = torch.empty(2, 8, 4, device="cuda")
+    with pytest.raises(ValueError):
+        selinv.selective_scan(*args, out={"state": state, "y": state.view(-1)[:1].expand(2, 6, 8)})
+    flat = torch.empty(2 * 6 * 8 + 10, device="cuda")
+    with pytest.raises(ValueError):
+        selinv.causal_conv(v["x"], torch.ones(8, 4, device="cuda"),
+                           out={"y": flat[:96].view(2, 6, 8), "state": flat[58:106].view(2, 3, 8)})
+
+
+def test_offsets_beyond_32_bits(cuda_ok):
+    """A cache of more than 2^31 elements, and rows and lines that lie as far apart: the same results as close by."""
+    big = torch.empty(2 ** 31 + 2 ** 29 + 2 ** 21, device="cuda")
+    v, yb, _ = scan_inputs(19, torch.float32, (3, 2), 64, 16, 1)
+    args = [v["x"], v["dt"], v["A"], v["B"], v["C"]]
+    far = big.as_strided((3, 2, 64), (2 ** 30, 2 ** 29, 1)).copy_(v["x"])
+    r, s = (selinv.selective_scan(x, *args[1:], z=v["z"], keep=True) for x in (v["x"], far))
+    assert torch.equal(r["y"], s["y"]) and torch.equal(r["state"], s["state"])
+    out = {"xb": far}
+    b = selinv.selective_scan_backward(r["kept"], *args, yb, z=v["z"])
+    selinv.selective_scan_backward(r["kept"], *args, yb, z=v["z"], out=out)
+    assert torch.equal(b["xb"], far)
+    w = torch.randn(64, 4, device="cuda")
+    far.copy_(v["x"])
+    assert torch.equal(selinv.causal_conv(far, w)["y"], selinv.causal_conv(v["x"], w)["y"])
+    x, dt, z, B, C = (v[k][:, 0].contiguous() for k in ("x", "dt", "z", "B", "C"))
+    for shape, step in (((64, 16), lambda c, i: selinv.selective_scan_step(c, x, dt, v["A"], B, C, z=z, index=i)),
+                        ((3, 64), lambda c, i: selinv.causal_conv_step(c, x, w, index=i))):
+        size = shape[0] * shape[1]
+        slots = big.numel() // size
+        cache, near_by = big[:slots * size].view(slots, *shape), torch.randn(3, *shape, device="cuda")
+        at = torch.tensor([slots - 1, 1, slots - 2], dtype=torch.int32, device="cuda")
+        cache[at.long()] = near_by
+        y = step(near_by, torch.arange(3, dtype=torch.int32, device="cuda"))
+        assert torch.equal(step(cache, at), y) and torch.equal(cache[at.long()], near_by)
