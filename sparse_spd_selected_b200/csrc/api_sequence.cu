@@ -55,11 +55,11 @@ bool wide(const selinv_view &v, size_t es, int64_t group, size_t pack = 16)
 }
 In in_of(const selinv_view &v, size_t es, int64_t group, size_t pack = 16)
 {
-    return In{v.data, v.line, (int)v.row, wide(v, es, group, pack)};
+    return In{v.data, v.line, (int)v.row, wide(v, es, group, pack), wide(v, es, group, es < 4 ? 4 : es)};
 }
 Out out_of(const selinv_view &v, size_t es, int64_t group)
 {
-    return Out{const_cast<void *>(v.data), v.line, (int)v.row, wide(v, es, group)};
+    return Out{const_cast<void *>(v.data), v.line, (int)v.row, wide(v, es, group), wide(v, es, group, es < 4 ? 4 : es)};
 }
 
 selinv_status rows_check(int64_t lines, int64_t rows, const int64_t *table, int64_t sequences, int64_t live)
@@ -187,6 +187,7 @@ selinv_status scan_args(const selinv_scan_inputs &a, const Spread &s, ScanArgs &
     p.A = a.A, p.D = a.D, p.dt_bias = a.dt_bias, p.state = a.state;
     p.segs = s.segs, p.seg_rows = (int)s.seg_rows;
     p.ends_lanes = s.lanes;
+    p.sms = sm_count();
     return SELINV_OK;
 }
 

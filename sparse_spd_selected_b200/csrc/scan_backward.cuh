@@ -330,10 +330,10 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
     const bool full = p.x.wide && p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.B.wide && p.C.wide && w.nch == CW && whole_n<T>(n);
     auto fetch_as = [&](auto whole, int r) {
         constexpr bool F = whole.value;
-        raw_fetch<CW, F>(sm.x, x, p.x.row, r, w.r1, w.nch, p.x.wide, lane);
-        raw_fetch<CW, F>(sm.dt_raw, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
-        raw_fetch<CW, F>(sm.yb_raw, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
-        if (z) raw_fetch<CW, F>(sm.z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
+        raw_fetch<CW, F>(sm.x, x, p.x, r, w.r1, w.nch, lane);
+        raw_fetch<CW, F>(sm.dt_raw, dt, p.dt, r, w.r1, w.nch, lane);
+        raw_fetch<CW, F>(sm.yb_raw, yb, o.yb, r, w.r1, w.nch, lane);
+        if (z) raw_fetch<CW, F>(sm.z, z, p.z, r, w.r1, w.nch, lane);
         raw_fetch_n<SCAN_WARPS * 32, F>(block.b_raw, B, p.B.row, r, w.r1, n, p.B.wide, threadIdx.x);
         raw_fetch_n<SCAN_WARPS * 32, F>(block.c_raw, Cc, p.C.row, r, w.r1, n, p.C.wide, threadIdx.x);
         cp_async_commit();
@@ -565,9 +565,9 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
     const bool full = p.dt.wide && o.yb.wide && (!z || p.z.wide) && p.C.wide && w.nch == CW && whole_n<T>(p.n);
     auto fetch_as = [&](auto whole, int r, int to) {
         constexpr bool F = whole.value;
-        raw_fetch<CW, F>(sm.raw[to].dt, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
-        raw_fetch<CW, F>(sm.raw[to].yb, yb, o.yb.row, r, w.r1, w.nch, o.yb.wide, lane);
-        if (z) raw_fetch<CW, F>(sm.raw[to].z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
+        raw_fetch<CW, F>(sm.raw[to].dt, dt, p.dt, r, w.r1, w.nch, lane);
+        raw_fetch<CW, F>(sm.raw[to].yb, yb, o.yb, r, w.r1, w.nch, lane);
+        if (z) raw_fetch<CW, F>(sm.raw[to].z, z, p.z, r, w.r1, w.nch, lane);
         raw_fetch_n<32, F>(sm.raw[to].c, Cc, p.C.row, r, w.r1, p.n, p.C.wide, lane);
         cp_async_commit();
     };

@@ -67,8 +67,11 @@ SELINV_DEVINL typename K::C scan_row(const ScanFwdSmem<K> &sm, int t, int dl, in
 }
 
 // MAIN: outputs.  Otherwise only what each segment leaves behind: its end state from a zero state, its sum of steps.
-template <class K, bool MAIN>
-__global__ void __launch_bounds__(SCAN_WARPS * 32) scan_kernel(const __grid_constant__ ScanArgs p)
+// BLOCKS per SM that the registers are kept to.  Four (128 registers), as many as segments are planned for, where they
+// fill the GPU (4096 x 2048 x 16: 121 us, 132 without); none where no more than two come to an SM, whose warps work
+// better with 168 (4 x 2048 x 4096 x 16: 358 us, 404 with).
+template <class K, bool MAIN, int BLOCKS>
+__global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __grid_constant__ ScanArgs p)
 {
     using T = typename K::T;
     using C = typename K::C;
@@ -119,9 +122,9 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) scan_kernel(const __grid_cons
     const bool full = p.x.wide && p.dt.wide && (!z || p.z.wide) && p.B.wide && p.C.wide && w.nch == CW && whole_n<T>(p.n);
     auto fetch_as = [&](auto whole, int r, int to) {
         constexpr bool F = whole.value;
-        raw_fetch<CW, F>(sm.raw[to].x, x, p.x.row, r, w.r1, w.nch, p.x.wide, lane);
-        raw_fetch<CW, F>(sm.raw[to].dt, dt, p.dt.row, r, w.r1, w.nch, p.dt.wide, lane);
-        if (MAIN && z) raw_fetch<CW, F>(sm.raw[to].z, z, p.z.row, r, w.r1, w.nch, p.z.wide, lane);
+        raw_fetch<CW, F>(sm.raw[to].x, x, p.x, r, w.r1, w.nch, lane);
+        raw_fetch<CW, F>(sm.raw[to].dt, dt, p.dt, r, w.r1, w.nch, lane);
+        if (MAIN && z) raw_fetch<CW, F>(sm.raw[to].z, z, p.z, r, w.r1, w.nch, lane);
         raw_fetch_n<32, F>(sm.raw[to].b, B, p.B.row, r, w.r1, p.n, p.B.wide, lane);
         if (MAIN) raw_fetch_n<32, F>(sm.raw[to].c, Cc, p.C.row, r, w.r1, p.n, p.C.wide, lane);
         cp_async_commit();
@@ -137,16 +140,15 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) scan_kernel(const __grid_cons
         raw_clear_n<32>(sm.raw[i].b, p.n, lane);
         if (MAIN) raw_clear_n<32>(sm.raw[i].c, p.n, lane);
     }
-    __syncwarp();
-    fetch(w.r0, 0);
     C total = 0;
 
-    for (int rt = w.r0; rt < w.r1; rt += R) {
+    for (int rt = w.r0 - R; rt < w.r1; rt += R) {       // the first time only to fetch: one place in the code that does
         const int at = ((rt - w.r0) / R) & 1;
         const ScanRaw<K> &raw = sm.raw[at];
         cp_async_wait_all();
         __syncwarp();
         if (rt + R < w.r1) fetch(rt + R, at ^ 1);
+        if (rt < w.r0) continue;
         raw_stage_n<32>(sm.b, raw.b, lane);
         if (MAIN) raw_stage_n<32>(sm.c, raw.c, lane);
         const int nr = min(R, w.r1 - rt);
@@ -252,6 +254,15 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) scan_kernel(const __grid_cons
     }
 }
 
+template <class K, bool MAIN, int BLOCKS>
+cudaError_t scan_start(const ScanArgs &p, const dim3 &grid, int threads, int bytes, cudaStream_t s)
+{
+    const cudaError_t e =
+        cudaFuncSetAttribute(scan_kernel<K, MAIN, BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    scan_kernel<K, MAIN, BLOCKS><<<grid, threads, bytes, s>>>(p);
+    return cudaGetLastError();
+}
 template <class K> cudaError_t scan_run(const ScanArgs &p, cudaStream_t s)
 {
     // float64 with many states: fewer warps fit
@@ -260,15 +271,13 @@ template <class K> cudaError_t scan_run(const ScanArgs &p, cudaStream_t s)
     static_assert(bytes <= 227 * 1024, "fits an SM");
     const int64_t per = p.d / p.groups, tiles = (per + K::CW - 1) / K::CW;
     const dim3 grid((unsigned)(p.lines * p.segs), (unsigned)(p.groups * ((tiles + warps - 1) / warps)));
+    constexpr int full = sizeof(typename K::C) == 4 ? 4 : 1;
     if (p.segs > 1) {
-        cudaError_t e = cudaFuncSetAttribute(scan_kernel<K, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const cudaError_t e = scan_start<K, false, full>(p, grid, warps * 32, bytes, s);
         if (e != cudaSuccess) return e;
-        scan_kernel<K, false><<<grid, warps * 32, bytes, s>>>(p);
     }
-    cudaError_t e = cudaFuncSetAttribute(scan_kernel<K, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    scan_kernel<K, true><<<grid, warps * 32, bytes, s>>>(p);
-    return cudaGetLastError();
+    if (full > 1 && (int64_t)grid.x * grid.y <= 2 * p.sms) return scan_start<K, true, 1>(p, grid, warps * 32, bytes, s);
+    return scan_start<K, true, full>(p, grid, warps * 32, bytes, s);
 }
 
 // Calls f with the tile of NP states and so many lanes per channel.

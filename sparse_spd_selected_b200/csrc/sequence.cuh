@@ -386,12 +386,12 @@ struct Rows {
 };
 
 // An array [lines, rows, channels]: strides in elements, channels contiguous.  `wide`: base, strides and the first
-// channel of every group lie on 16 bytes, so that packs may be moved whole.
+// channel of every group lie on 16 bytes, so that packs may be moved whole; `words`: on 4 (8 in float64).
 template <class P> struct Strided {
     P p;
     int64_t line;
     int row;
-    bool wide;
+    bool wide, words;
 };
 using In = Strided<const void *>;
 using Out = Strided<void *>;
@@ -408,6 +408,7 @@ struct ScanArgs {
     void *state_out, *kept;     // may be null
     // lines cut into segments of seg_rows rows: the state each leaves behind from zero, and the sum of its steps
     int segs, seg_rows;
+    int sms;                    // multiprocessors of the device
     int ends_lanes;             // lanes per channel of the backward's run over the segments' ends
     void *ends, *sums;
 };
