@@ -104,7 +104,7 @@ Spread scan_spread(const selinv_scan_inputs &a, bool backward)
     int64_t cw = backward ? with_type(a.dtype, [&](auto t) { return scan_backward_channels<decltype(t)>(n); }) : 32 / s.lanes;
     // A line that is cut is run twice but for its last segment, first for the states that segments leave behind.  So it
     // is cut only where its blocks come to less than about one per SM (forward; 128 blocks of 4 x 2048 x 4096 x 16 take
-    // 354 us whole, 350 in 16 segments) or to less than 0.7 of those resident (backward; with two resident per SM 128
+    // 306 us whole, 366 in 16 segments) or to less than 0.7 of those resident (backward; with two resident per SM 128
     // blocks take 1297 us whole and 994 in 8 segments, 256 blocks 895 whole and 965 in 4).
     const int64_t resident =
         (backward ? with_type(a.dtype, [&](auto t) { return scan_backward_blocks<decltype(t)>(n); }) : 4) * sms;
@@ -121,6 +121,11 @@ Spread scan_spread(const selinv_scan_inputs &a, bool backward)
         if (segs > a.rows / 64) segs = a.rows / 64;
         if (b * segs < 2 * sms) segs = 2 * sms / b < a.rows / 32 ? 2 * sms / b : a.rows / 32;
         s.segs = (int)(segs < 1 ? 1 : segs < MAX_SEGS ? segs : MAX_SEGS);
+    } else if (!backward && s.lanes == 1 && scan_most_lanes(n) > 1 && 2 * blocks(cw) <= 3 * sms) {
+        // Whole lines, one or two blocks per SM: twice the warps of half the channels hide more of each other's waits
+        // and spread more evenly (x 1024 x 4096 x 16: 4 lines 184 us with one lane, 158 with two; 5 lines 256 and 206;
+        // 7 lines 257 either way, 12 lines 367 and 386).
+        s.lanes = 2, cw = 16;
     }
     // the backward's run over the segments' ends: lanes until there are three blocks per SM
     if (backward)

@@ -413,7 +413,7 @@ SELINV_DEVINL bool step_first(const int32_t *index, int32_t *info, int64_t r, in
     if (!index) return true;
     bool twice = false;
     if (slot >= 0)
-        for (int64_t i = threadIdx.x; i < r; i += blockDim.x) twice |= index[i] == slot;
+        for (int i = threadIdx.x; i < (int)r; i += blockDim.x) twice |= index[i] == (int)slot;
     twice = __syncthreads_or(twice);
     if (reports && info && threadIdx.x == 0)
         info[r] = twice ? STEP_TWICE : slot < 0 && index[r] != -1 ? STEP_RANGE : STEP_OK;
@@ -425,8 +425,9 @@ template <class T, int K>
 __global__ void __launch_bounds__(CONV_THREADS) conv_step_kernel(const __grid_constant__ ConvStepArgs p)
 {
     using C = typename Elem<T>::C;
-    const int64_t blocks = (p.d + CONV_THREADS - 1) / CONV_THREADS, r = blockIdx.x / blocks;
-    const int64_t c = (blockIdx.x % blocks) * CONV_THREADS + threadIdx.x;
+    const unsigned blocks = (unsigned)((p.d + CONV_THREADS - 1) / CONV_THREADS), row = blockIdx.x / blocks;
+    const int64_t r = row;
+    const int c = (int)(blockIdx.x - row * blocks) * CONV_THREADS + threadIdx.x;
     const int64_t slot = step_slot(p.index, r, p.slots);
     const bool in = c < p.d;
     T win[K];
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_step_kernel(const __grid_co
 #pragma unroll
         for (int j = 0; j < K; ++j) wt[j] = Elem<T>::up(static_cast<const T *>(p.weight)[c * K + j]);
     }
-    const bool ours = step_first(p.index, p.info, r, slot, blockIdx.x % blocks == 0);
+    const bool ours = step_first(p.index, p.info, r, slot, blockIdx.x == row * blocks);
     if (!in) return;
     C v = bias;
 #pragma unroll

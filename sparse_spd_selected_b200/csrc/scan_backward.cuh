@@ -23,7 +23,7 @@
 // each other's waits (0.45 instructions a cycle).  4 x 2048 x 4096 x 16 in
 // bfloat16: 963 us, of which 178 the run over the segments' ends and 13 the
 // partial sums, against 137 us for the powers of two and sigmoids of one pass
-// and 62 us of memory.  Keeping the first run's powers for the second would take
+// and 92 us of memory.  Keeping the first run's powers for the second would take
 // 32 KB a warp, and so half of the warps.
 #pragma once
 
@@ -237,8 +237,8 @@ template <class K> struct ScanBwd {
 };
 
 // Blocks per SM that shared memory and registers allow; three keep to 168 registers, where eight states would spill (16
-// states: in 16-bit types 963 us with eight and two blocks, 1036 with four and three, 4 x 2048 x 4096; in float 175 and
-// 141, 3 x 517 x 1250).
+// states: in 16-bit types 963 us with eight and two blocks, 1036 with four and three, 4 x 2048 x 4096; in float four are
+// a fifth faster, 3 x 517 x 1250).
 template <class K> constexpr int scan_bwd_blocks = K::SN <= 4 && 3 * (sizeof(ScanBwdBlock<K>) + 1024) <= 228 * 1024   ? 3
                                                    : 2 * (sizeof(ScanBwdBlock<K>) + 1024) <= 228 * 1024 ? 2
                                                                                                         : 1;

@@ -7,13 +7,13 @@
 // with x, a second one the states and the sums of y, a third one the outputs.
 // What bounds it is the special function unit: one power of two per row,
 // channel and state, 16 a cycle and SM, and three more per row and
-// channel (one with the softplus, two with z).  4 x 2048 x 4096 x 16 in bfloat16: 375 us for 5.4e8 states, 137 us of
-// that unit alone (65 to 75 % of it busy while all warps run) and 54 us of
-// memory; one warp alone keeps it half busy, four per scheduler do not hide
-// every wait.  A polynomial for a part of the powers on the FMA pipe gave
-// nothing (its issue slots are the next bound).  Cut into segments (one line of
-// 8192 x 1024 x 16: 117 us, 46 of them the summary run) the powers are formed
-// twice; joining the segments in batches of four took 125, for its registers.
+// channel (one with the softplus, two with z).  4 x 2048 x 4096 x 16 in bfloat16,
+// states kept: 306 us for 5.4e8 states, 137 us of that unit alone and 62 us of
+// memory; one or two warps per scheduler do not keep it busy.  Cut into segments
+// (one line of 4096 x 2048 x 16: 117 us, 46 of them the summary run) it is 65 to
+// 75 % busy, but the powers are formed twice.  A polynomial for a part of the
+// powers on the FMA pipe gave nothing (issue slots are the next bound), joining
+// the segments in batches of four took 125 us, for its registers.
 #pragma once
 
 #include "scan.cuh"
@@ -69,7 +69,7 @@ SELINV_DEVINL typename K::C scan_row(const ScanFwdSmem<K> &sm, int t, int dl, in
 // MAIN: outputs.  Otherwise only what each segment leaves behind: its end state from a zero state, its sum of steps.
 // BLOCKS per SM that the registers are kept to.  Four (128 registers), as many as segments are planned for, where they
 // fill the GPU (4096 x 2048 x 16: 121 us, 132 without); none where no more than two come to an SM, whose warps work
-// better with 168 (4 x 2048 x 4096 x 16: 358 us, 404 with).
+// better with all they want (4 x 2048 x 4096 x 16, one lane: 358 us, 404 with).
 template <class K, bool MAIN, int BLOCKS>
 __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __grid_constant__ ScanArgs p)
 {

@@ -20,8 +20,9 @@ template <class T, int LN>
 __global__ void __launch_bounds__(STEP_THREADS) scan_step_kernel(const __grid_constant__ ScanStepArgs p)
 {
     using C = typename Elem<T>::C;
-    const int blocks = (int)((p.d + STEP_THREADS - 1) / STEP_THREADS), bi = (int)(blockIdx.x % blocks);
-    const int64_t r = blockIdx.x / blocks;
+    const unsigned blocks = (unsigned)((p.d + STEP_THREADS - 1) / STEP_THREADS), row = blockIdx.x / blocks;
+    const int bi = (int)(blockIdx.x - row * blocks);
+    const int64_t r = row;
     const int64_t slot = step_slot(p.index, r, p.slots);
     const int lane = threadIdx.x % 32, nl = threadIdx.x % LN, n0 = nl * 4, n = p.n, d = (int)p.d;
     const int c = bi * STEP_THREADS + threadIdx.x, first = c - nl;      // this lane's channel, and its lanes' first
@@ -30,12 +31,14 @@ __global__ void __launch_bounds__(STEP_THREADS) scan_step_kernel(const __grid_co
                       ((uintptr_t)p.cache | (uintptr_t)p.cache_out | (uintptr_t)p.A) % 16 == 0;
     constexpr int U = LN < 4 ? LN : 4;          // channels whose loads are on their way together
     C h[U][4], a[U][4];
+    const int64_t at = (slot * d + first) * n + n0;     // the lane's states of its first channel
+    const C *const hs0 = static_cast<const C *>(p.cache) + at, *const as0 = static_cast<const C *>(p.A) + ((int64_t)first * n + n0);
+    C *const out0 = static_cast<C *>(p.cache_out) + at;
     const auto load = [&](int u0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int ch = first + u0 + u;
-            const C *hs = static_cast<const C *>(p.cache) + (slot * d + ch) * n + n0;
-            const C *as = static_cast<const C *>(p.A) + (int64_t)ch * n + n0;
+            const C *hs = hs0 + (u0 + u) * n, *as = as0 + (u0 + u) * n;
             const bool have = slot >= 0 && ch < d && n0 < n;
             if (have && wide) {
                 get<4>(hs, h[u]);
@@ -64,7 +67,7 @@ __global__ void __launch_bounds__(STEP_THREADS) scan_step_kernel(const __grid_co
         if (in) *y = Elem<T>::down((C)0);
         return;
     }
-    const int per = d / p.groups;
+    const int per = p.groups == 1 ? d : d / p.groups;
     C b[4], cc[4], v[LN];
     int group = -1;
     if (p.softplus) dt = softplus_(dt);
@@ -75,7 +78,7 @@ __global__ void __launch_bounds__(STEP_THREADS) scan_step_kernel(const __grid_co
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int ch = first + u0 + u, from = lane - nl + u0 + u;
-            const int g = ch < d ? ch / per : group;
+            const int g = ch >= d ? group : p.groups == 1 ? 0 : ch / per;
             if (g != group) {       // once in a call with one group
                 group = g;
                 const T *B = static_cast<const T *>(p.B) + r * p.B_row + g * p.B_group + n0;
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(STEP_THREADS) scan_step_kernel(const __grid_co
                     v[u0 + u] += cc[j] * h[u][j];
                 }
             if (ch < d && n0 < n) {
-                C *out = static_cast<C *>(p.cache_out) + (slot * d + ch) * n + n0;
+                C *out = out0 + (u0 + u) * n;
                 if (wide) {
                     put<4>(out, h[u]);
                 } else {
