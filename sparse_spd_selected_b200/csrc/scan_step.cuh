@@ -3,9 +3,9 @@
 // Each lane has a channel of its own for what a channel has once (step, gate,
 // y); for the states LN neighbouring lanes take their LN channels one after
 // another, four states of each a lane, so that the loads and stores of 16
-// bytes cover whole sectors.  192 rows of 4096 x 16: 29 us for 107 MB, 3.7 TB/s
-// (0.57 of a plain copy's rate, the time of a launch included); one row of 1024 x 16: 4.7 us,
-// a launch and two waits for memory.
+// bytes cover whole sectors.  192 rows of 4096 x 16: 28 us for 107 MB, 3.8 TB/s
+// (0.58 of a plain copy's rate); held to 64 registers for eight blocks per SM it
+// took 30.  One row of 2048 x 16: 4.7 us, a launch and two waits for memory.
 #pragma once
 
 #include "conv.cuh"
