@@ -134,6 +134,20 @@ def test_scan_wide_tiles(cuda_ok, kind, d, n):
     check_scan(200 + n, kind, [18] * 8, d, n, groups=1 if d % 2 else 2, with_state=True)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f64"])
+@pytest.mark.parametrize("lines,n", [(37, 16), (50, 12), (50, 7)])
+def test_scan_whole_lines(cuda_ok, kind, lines, n):
+    """Lines that are not cut, one or two blocks per multiprocessor, of channels that end within a tile."""
+    check_scan(52, kind, [18] * lines, 490, n)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("d,groups", [(34, 1), (35, 1), (70, 2), (68, 2), (1, 1)])
+def test_scan_rows_off_16_bytes(cuda_ok, kind, d, groups):
+    """Rows of 16-bit elements on words and on odd places, and channels that end in the middle of a word."""
+    check_scan(53, kind, [19, 19], d, 16, groups)
+
+
 @pytest.mark.parametrize("kind", ["f32", "f16", "f64"])
 @pytest.mark.parametrize("rows,d,n", [(700, 8, 16), (1030, 33, 5), (257, 16, 64), (130, 3, 4)])
 def test_scan_segments(cuda_ok, kind, rows, d, n):
