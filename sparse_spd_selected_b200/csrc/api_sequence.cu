@@ -171,7 +171,7 @@ ScanSpace scan_space(const selinv_scan_inputs &a, const Spread &s, bool backward
 size_t scan_workspace(const selinv_scan_inputs *a, bool backward)
 {
     if (!a || !valid(a->dtype) || a->d < 1 || a->d > MAX_D || a->n < 1 || a->n > SCAN_MAX_N || a->groups < 1 ||
-        a->d % a->groups || a->lines < 1 || a->rows < 1)
+        a->d % a->groups || a->lines < 1 || a->rows < 0 || (a->rows == 0 && !a->table))
         return 0;
     return scan_space(*a, scan_spread(*a, backward), backward).total;
 }
