@@ -43,7 +43,7 @@ template <int E> SELINV_DEVINL bool conv_place(const ConvArgs &p, ConvPlace &w)
     w.line = rest / p.chunks;
     w.chunk = (int)(rest % p.chunks);
     w.r0 = w.chunk * p.chunk_rows;
-    w.r1 = min(p.rows.rows, w.r0 + p.chunk_rows);
+    w.r1 = piece_end(w.r0, p.chunk_rows, p.rows.rows);
     return true;
 }
 

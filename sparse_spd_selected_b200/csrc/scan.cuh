@@ -270,7 +270,7 @@ SELINV_DEVINL bool scan_place(const ScanArgs &p, int warp, int warps, int cw, Sc
     w.group = (int)blockIdx.y / blocks;
     const int tile = ((int)blockIdx.y % blocks) * warps + warp;
     w.r0 = w.seg * p.seg_rows;
-    w.r1 = min(p.rows.rows, w.r0 + p.seg_rows);
+    w.r1 = piece_end(w.r0, p.seg_rows, p.rows.rows);
     w.c0 = w.group * per + tile * cw;
     w.nch = min(cw, per - tile * cw);
     return w.nch > 0;

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "pieces.h"
 
 namespace selinv {
 
@@ -358,7 +359,7 @@ struct Rows {
         if (!table) return 0;
         int lo = 0, hi = live;
         while (hi - lo > 1) {
-            const int m = (lo + hi) / 2;
+            const int m = lo + (hi - lo) / 2;
             if (table[m] <= r)
                 lo = m;
             else

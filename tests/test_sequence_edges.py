@@ -1,4 +1,6 @@
 """Edges of the sequence operators that need no GPU: buffer sizes, refusals and the arithmetic of rows at the limits."""
+import subprocess
+
 import pytest
 import torch
 
@@ -21,3 +23,34 @@ def test_backward_workspace_of_sequences_without_rows(lib):
     v = [FAKE] + [0] * 3 + [0] + [0] * 15 + [0, 0] + [FAKE, 0, 0, 0]
     assert lib.selinv_selective_scan_backward(empty, selinv._SCAN_GRADS.pack(*v), FAKE, size(empty) - 1, 0) == \
         selinv.ERR_WORKSPACE
+
+
+def test_pieces_end_within_the_line(tmp_path):
+    """Segments and chunks cover a line up to the most rows that one may have, whatever their length."""
+    src = tmp_path / "pieces.cpp"
+    src.write_text("""
+#include <cstdio>
+#include <initializer_list>
+#include "pieces.h"
+int main()
+{
+    long long bad = 0;
+    for (int rows : {0x7fffffff - 64, 0x7fffffff - 65, 0x7fffffff - 200, 0x7fffffff - 2600, 1000, 1})
+        for (int pieces = 1; pieces <= 160; ++pieces)
+            for (int round : {4, 16, 128}) {
+                const long long step = ((1LL * rows + pieces - 1) / pieces + round - 1) / round * round;
+                long long at = 0;
+                for (long long r0 = 0; r0 < rows; r0 += step) {
+                    const int end = selinv::piece_end((int)r0, (int)(step < 0x7fffffff ? step : 0x7fffffff), rows);
+                    bad += r0 != at || end <= r0 || end - r0 > step;
+                    at = end;
+                }
+                bad += at != rows;
+            }
+    printf("%lld\\n", bad);
+}
+""")
+    exe = tmp_path / "pieces"
+    subprocess.check_call(["g++", "-std=c++17", "-fsanitize=signed-integer-overflow", "-fno-sanitize-recover", "-I",
+                           build.CSRC, str(src), "-o", str(exe)])
+    assert subprocess.check_output([str(exe)]).decode().strip() == "0"

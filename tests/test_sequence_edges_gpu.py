@@ -39,3 +39,46 @@ def test_gradients_of_sequences_without_rows(cuda_ok):
     assert torch.equal(v["state"].grad, stateb)
     for k in ("A", "D", "dt_bias"):
         assert not v[k].grad.any(), k
+
+
+MOST_ROWS = 2 ** 31 - 65
+
+
+def repeated(value, *shape):
+    return torch.full((1,) * len(shape), value, dtype=torch.float16, device="cuda").expand(*shape)
+
+
+@pytest.mark.parametrize("rows", [MOST_ROWS, MOST_ROWS - 1400])
+def test_scan_of_the_longest_lines(cuda_ok, rows):
+    """One channel and one state over as many rows as a line may have: every row is written, and the final state.  The
+    inputs are one row, repeated: h = a h + u with a = 1/2, u = 1/4, B = C = 1, so y is 1/2 but for the first rows."""
+    x, dt, one = repeated(0.25, rows, 1), repeated(1.0, rows, 1), repeated(1.0, rows, 1, 1)
+    A = torch.full((1, 1), -float(np.log(2.0)), device="cuda")
+    out = {"y": torch.full((rows, 1), float("nan"), dtype=torch.float16, device="cuda")}
+    r = selinv.selective_scan(x, dt, A, one, one, out=out)
+    y = out["y"]
+    # a is off by some units of float, y's last rounding is half a unit of float16
+    assert abs(float(r["state"]) - 0.5) < 1e-6
+    assert float((y[64:] - 0.5).abs().max()) <= 2.0 ** -11 and bool(torch.isfinite(y[:64]).all())
+
+
+@pytest.mark.parametrize("rows", [MOST_ROWS, MOST_ROWS - 63])
+def test_conv_of_the_longest_lines(cuda_ok, rows):
+    """One channel over as many rows as a line may have, forward and backward; all sums are exact but weightb's."""
+    x = repeated(0.5, rows, 1)
+    w = torch.tensor([[1.0, 2.0, -4.0]], dtype=torch.float16, device="cuda")
+    out = {"y": torch.full((rows, 1), float("nan"), dtype=torch.float16, device="cuda")}
+    state = torch.full((2, 1), 0.25, dtype=torch.float16, device="cuda")
+    r = selinv.causal_conv(x, w, state=state, out=out)
+    assert bool((out["y"][2:] == -0.5).all()) and out["y"][:2, 0].tolist() == [-1.25, -0.75]
+    assert r["state"][:, 0].tolist() == [0.5, 0.5]
+    out = {"xb": out["y"].fill_(float("nan"))}
+    b = selinv.causal_conv_backward(x, w, repeated(0.25, rows, 1), state=state, out=out)
+    assert bool((out["xb"][:-2] == -0.25).all()) and out["xb"][-2:, 0].tolist() == [-0.5, -1.0]
+    assert b["stateb"][:, 0].tolist() == [0.25, 0.75]
+    # the sums: rows of 1/8 (less the states' rows), in chunks of at most 128 rows and 8 strands of those
+    count = -(-rows // 128)
+    bound = (128 + count / 8 + 8) * 2.0 ** -24
+    ref = np.array([[2 * 0.25 * 0.25 + (rows - 2) * 0.125, 0.25 * 0.25 + (rows - 1) * 0.125, rows * 0.125]])
+    assert (np.abs(host(b["weightb"]) - ref) <= bound * ref).all()
+    assert abs(float(b["biasb"]) - 0.25 * rows) <= bound * 0.25 * rows
