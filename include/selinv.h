@@ -498,7 +498,7 @@ selinv_status selinv_tree_backward(const selinv_tree_plan_t *plan, selinv_dtype 
  *     alignment of base and strides enables the vectorised paths.  A stride
  *     between rows is below 2^31 (SELINV_ERR_INVALID_ARG beyond), a line has
  *     at most 2^31 - 65 rows; SELINV_ERR_UNSUPPORTED for more, and for more
- *     lines x segments or groups x channel tiles than a grid holds.
+ *     lines x segments or groups x blocks of channels (four tiles each) than a grid holds.
  *   - Without a table each line is one sequence of `rows` rows.  With a table
  *     there is one line, holding the sequences one after another: `table`
  *     (device, int64, 1 + live + sequences entries) has the first rows of the

@@ -93,7 +93,7 @@ selinv_status scan_check(const selinv_scan_inputs &a)
 // How a scan is spread over the GPU.
 struct Spread {
     int lanes, segs;                        // lanes of a channel (forward), segments of a line
-    int64_t seg_rows, tiles, blocks;        // tiles of a warp's channels and blocks of tiles, over all groups
+    int64_t seg_rows, blocks, ends_blocks;  // blocks over all groups' channels; of the backward's run over segment ends
 };
 Spread scan_spread(const selinv_scan_inputs &a, bool backward)
 {
@@ -130,8 +130,8 @@ Spread scan_spread(const selinv_scan_inputs &a, bool backward)
     // the backward's run over the segments' ends: lanes until there are three blocks per SM
     if (backward)
         while (s.lanes < scan_most_lanes(n) && blocks(32 / s.lanes) * s.segs < 3 * sms) s.lanes *= 2;
-    s.tiles = a.groups * div_up(per, cw);
     s.blocks = a.groups * div_up(div_up(per, cw), SCAN_BLOCK_TILES);
+    s.ends_blocks = backward ? a.groups * div_up(div_up(per, 32 / s.lanes), SCAN_BLOCK_TILES) : 0;
     s.seg_rows = div_up(div_up(a.rows, s.segs), SCAN_KEEP_ROWS) * SCAN_KEEP_ROWS;
     if (s.seg_rows < SCAN_KEEP_ROWS) s.seg_rows = SCAN_KEEP_ROWS;
     s.segs = (int)div_up(a.rows, s.seg_rows);
@@ -180,7 +180,7 @@ selinv_status scan_args(const selinv_scan_inputs &a, const Spread &s, ScanArgs &
 {
     const size_t es = elem(a.dtype);
     const int64_t per = a.groups > 1 ? a.d / a.groups : 0;
-    if (a.lines * s.segs > MAX_GRID_X || s.tiles > MAX_GRID_Y) return SELINV_ERR_UNSUPPORTED;
+    if (a.lines * s.segs > MAX_GRID_X || s.blocks > MAX_GRID_Y || s.ends_blocks > MAX_GRID_Y) return SELINV_ERR_UNSUPPORTED;
     const size_t pack = es == 2 ? 8 : 16;        // B and C: four elements at a time, two in float64
     p.rows = Rows{a.table, (int)a.live, (int)a.rows};
     p.lines = a.lines, p.d = a.d, p.sequences = a.sequences;

@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
 }
 template <class K> cudaError_t scan_ends_run(const ScanArgs &p, const ScanGrads &o, cudaStream_t s)
 {
-    constexpr int warps = SCAN_WARPS * sizeof(ScanEndsSmem<K>) <= 227 * 1024 ? SCAN_WARPS : SCAN_WARPS / 2;
+    constexpr int warps = SCAN_WARPS;
     constexpr int bytes = warps * (int)sizeof(ScanEndsSmem<K>);
     static_assert(bytes <= 227 * 1024, "fits an SM");
     const int64_t tiles = (p.d / p.groups + K::CW - 1) / K::CW;

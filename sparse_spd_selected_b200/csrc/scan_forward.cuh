@@ -265,8 +265,7 @@ cudaError_t scan_start(const ScanArgs &p, const dim3 &grid, int threads, int byt
 }
 template <class K> cudaError_t scan_run(const ScanArgs &p, cudaStream_t s)
 {
-    // float64 with many states: fewer warps fit
-    constexpr int warps = SCAN_WARPS * sizeof(ScanFwdSmem<K>) <= 227 * 1024 ? SCAN_WARPS : SCAN_WARPS / 2;
+    constexpr int warps = SCAN_WARPS;
     constexpr int bytes = warps * (int)sizeof(ScanFwdSmem<K>);
     static_assert(bytes <= 227 * 1024, "fits an SM");
     const int64_t per = p.d / p.groups, tiles = (per + K::CW - 1) / K::CW;

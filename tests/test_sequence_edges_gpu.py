@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from sparse_spd_selected_b200 import selinv
-from tests.test_sequence_gpu import TYPES, arith, dev, host, scan_inputs, unit
+from tests import sequence_plain as plain
+from tests.test_sequence_gpu import TYPES, arith, dev, host, near, scan_inputs, unit
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +83,32 @@ def test_conv_of_the_longest_lines(cuda_ok, rows):
     ref = np.array([[2 * 0.25 * 0.25 + (rows - 2) * 0.125, 0.25 * 0.25 + (rows - 1) * 0.125, rows * 0.125]])
     assert (np.abs(host(b["weightb"]) - ref) <= bound * ref).all()
     assert abs(float(b["biasb"]) - 0.25 * rows) <= bound * 0.25 * rows
+
+
+@pytest.mark.parametrize("kind,n,groups", [("bf16", 16, 1), ("f32", 32, 1), ("bf16", 64, 1), ("f32", 64, 4), ("f64", 32, 1)])
+def test_scan_of_the_widest_layers(cuda_ok, kind, n, groups):
+    """2^20 channels, forward and backward, at one row without a state: h = dt' x B in closed form."""
+    t, d = TYPES[kind], 2 ** 20
+    g = torch.Generator("cuda").manual_seed(n)
+    x, dt, yb = (torch.randn(1, d, generator=g, device="cuda").to(t) for _ in range(3))
+    B, C = (torch.randn(1, groups, n, generator=g, device="cuda").to(t) for _ in range(2))
+    A, D = -torch.ones(d, n, dtype=arith(t), device="cuda"), torch.ones(d, dtype=arith(t), device="cuda")
+    r = selinv.selective_scan(x, dt, A, B, C, D, softplus=True, keep=True)
+    b = selinv.selective_scan_backward(r["kept"], x, dt, A, B, C, yb, D=D, softplus=True)
+    x, dt, yb, B, C = (host(a)[0] for a in (x, dt, yb, B, C))
+
+    def closed(f):
+        step, slope = np.logaddexp(dt, 0), plain.sigmoid(dt)
+        xs, ys, bs, cs = f(x), f(yb), f(B), f(C)
+        bc = np.repeat((bs * cs).sum(1), d // groups)
+        per = lambda v: v.reshape(groups, -1).sum(1)[:, None]      # noqa: E731
+        return {"y": (bc * step + 1) * xs, "xb": (step * bc + 1) * ys, "dtb": xs * bc * ys * slope,
+                "Bb": cs * per(ys * step * xs), "Cb": bs * per(ys * step * xs),
+                "state": (step * xs)[-1000:, None] * bs[-1]}
+
+    ref, mag = closed(lambda v: v), closed(np.abs)
+    u = unit(arith(t))
+    for k, got, width in (("y", r["y"][0], 0), ("state", r["state"][-1000:], 0), ("xb", b["xb"][0], 0), ("dtb", b["dtb"][0], 0),
+                          ("Bb", b["Bb"][0], d), ("Cb", b["Cb"][0], d)):
+        near(k, got, ref[k], mag[k], plain.scan_bound(1, n, width, u))
+    assert not b["Ab"].any()
