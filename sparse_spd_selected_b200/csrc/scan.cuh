@@ -229,6 +229,14 @@ template <int N, class C> SELINV_DEVINL void store_states(C *p, int m, bool in, 
         if (2 * j + 1 < m) p[2 * j + 1] = v[j].y;
     }
 }
+// The J-th pair of a lane's states, of which m exist, with zeros for those that do not.  They have no inputs and are zero as
+// it is, but for infinities: an infinite step or input times their B of zero is not a number.
+template <class V> SELINV_DEVINL V real_states(V v, int J, int m)
+{
+    if (2 * J >= m) v.x = 0;
+    if (2 * J + 1 >= m) v.y = 0;
+    return v;
+}
 template <int N, class V> SELINV_DEVINL void zero_states(V *v)
 {
 #pragma unroll

@@ -104,8 +104,10 @@ template <class K> struct ScanBwd {
         v.load(&sm.x[t][c], 2, true);
         x = make2(v.get(0), v.get(1));
     }
-    // Row t: the state before it becomes the state after it; its decays.
-    SELINV_DEVINL void row(int t, const V (*A2)[KP], V (*h)[KP], V (*a)[KP]) const
+    // How many of this lane's states channel i of its two has.
+    SELINV_DEVINL int real(int i) const { return c + i < nch ? p.n - n0 : 0; }
+    // Row t: the state before it becomes the state after it; its decays.  REAL: with zeros for what does not exist.
+    template <bool REAL> SELINV_DEVINL void row(int t, const V (*A2)[KP], V (*h)[KP], V (*a)[KP]) const
     {
         V dt, x, b[KP];
         inputs(t, dt, x);
@@ -117,6 +119,10 @@ template <class K> struct ScanBwd {
             a[1][j] = decay2(d1, A2[1][j]);
             h[0][j] = fma2(a[0][j], h[0][j], mul2(u0, b[j]));
             h[1][j] = fma2(a[1][j], h[1][j], mul2(u1, b[j]));
+            if (REAL) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) a[i][j] = real_states(a[i][j], j, real(i)), h[i][j] = real_states(h[i][j], j, real(i));
+            }
         }
     }
     // SCAN_S rows of the first run.  EDGE: some row begins a sequence.
@@ -126,16 +132,15 @@ template <class K> struct ScanBwd {
         for (int r = 0; r < SCAN_S; ++r) {
             V a[2][KP];
             if (EDGE && ((begins >> (t0 + r)) & 1u)) states(p.state, sequence(k0, begins, t0 + r), h);
-            row(t0 + r, A2, h, a);
+            row<false>(t0 + r, A2, h, a);
         }
     }
-    // Rows t0 .. t0 + SCAN_S - 1, `before` the state before them.  EDGE: some row begins or ends a sequence; st has the
+    // Rows t0 .. t0 + S - 1, `before` the state before them.  EDGE: some row begins or ends a sequence; st has the
     // rows that begin one and the row behind the last, of which only those below nr are rows.
-    template <bool EDGE>
+    template <int S, bool EDGE, bool REAL>
     SELINV_DEVINL void rows(int t0, int nr, uint32_t st, int k0, const V (*A2)[KP], const V (*before)[KP], V (*g)[KP],
                             V (*ab)[KP]) const
     {
-        constexpr int S = SCAN_S;
         const uint32_t begins = st & ((1u << nr) - 1u);
         V h[S][2][KP], a[S][2][KP];
 #pragma unroll
@@ -145,12 +150,17 @@ template <class K> struct ScanBwd {
 #pragma unroll
                 for (int j = 0; j < KP; ++j) h[r][i][j] = r ? h[r ? r - 1 : 0][i][j] : before[i][j];
             if (EDGE && ((begins >> (t0 + r)) & 1u)) states(p.state, sequence(k0, begins, t0 + r), h[r]);
-            row(t0 + r, A2, h[r], a[r]);
+            row<REAL>(t0 + r, A2, h[r], a[r]);
         }
 #pragma unroll
         for (int r = S - 1; r >= 0; --r) {
             const int t = t0 + r;
-            if (EDGE && ((st >> (t + 1)) & 1u)) states(o.stateb, sequence(k0, st, t), g);
+            if (EDGE && ((st >> (t + 1)) & 1u)) {
+                states(o.stateb, sequence(k0, st, t), g);
+                // A line's last row, the first that this block comes to but for up to three behind it that are none: their
+                // cotangents are zero, but zero times an infinite state is not a number.
+                if (t + 1 == nr && nr < SCAN_R) zero_states<SN>(ab[0]), zero_states<SN>(ab[1]);
+            }
             const bool first = EDGE && ((begins >> t) & 1u);
             V start[2][KP];
             if (EDGE) {
@@ -175,7 +185,8 @@ template <class K> struct ScanBwd {
 #pragma unroll
                 for (int j = 0; j < KP; ++j) {
                     const V past = EDGE ? start[i][j] : r > 0 ? h[r > 0 ? r - 1 : 0][i][j] : before[i][j];
-                    const V gt = fma2(c2[j], y2[i], g[i][j]);
+                    V gt = fma2(c2[j], y2[i], g[i][j]);
+                    if (REAL) gt = real_states(gt, j, real(i));
                     sb[j] = i ? fma2(gt, u2[i], sb[j]) : mul2(gt, u2[i]);
                     sc[j] = i ? fma2(h[r][i][j], y2[i], sc[j]) : mul2(h[r][i][j], y2[i]);
                     gb[i] = j ? fma2(gt, b[j], gb[i]) : mul2(gt, b[j]);
@@ -204,13 +215,62 @@ template <class K> struct ScanBwd {
                 out[SN + 2 * j] = sc[j].x, out[SN + 2 * j + 1] = sc[j].y;
             }
 #pragma unroll
-            for (int i = 0; i < K::CHUNKS; ++i) put<K::Q>(&sm.part[r % K::P][nl][i][lane % K::LD][0], out + i * K::Q);
+            for (int i = 0; i < K::CHUNKS; ++i) put<K::Q>(&sm.part[S > 1 ? r % K::P : t % K::P][nl][i][lane % K::LD][0], out + i * K::Q);
             if (first && o.stateb_out) store(static_cast<C *>(o.stateb_out) + p.rows.number(sequence(k0, st, t), line) * dn, g);
-            if (r % K::P == 0) {
+            if ((S > 1 ? r : t) % K::P == 0) {
                 __syncwarp();
                 sums(t);
                 __syncwarp();
             }
+        }
+    }
+    // The nr rows of a tile, from the state kept before them; begins and st as above.
+    SELINV_DEVINL void tile(const C *kept, int nr, uint32_t begins, uint32_t st, int k0, const V (*A2)[KP], V (*g)[KP],
+                            V (*ab)[KP]) const
+    {
+        constexpr int S = SCAN_S;
+        V h[2][KP];
+        load(kept, h);
+        for (int b = 0; b < SCAN_R / S - 1 && (b + 1) * S < nr; ++b) {
+            if ((begins >> (b * S)) & ((1u << S) - 1u))
+                skip<true>(b * S, begins, k0, A2, h);
+            else
+                skip<false>(b * S, begins, k0, A2, h);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < KP; ++j) sm.h[b][i * KP + j][lane] = h[i][j];
+        }
+        for (int b = (nr - 1) / S; b >= 0; --b) {
+            if (b > 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < KP; ++j) h[i][j] = sm.h[b - 1][i * KP + j][lane];
+            } else {
+                load(kept, h);
+            }
+            if ((st >> (b * S)) & ((2u << S) - 1u))
+                rows<S, true, false>(b * S, nr, st, k0, A2, h, g, ab);
+            else
+                rows<S, false, false>(b * S, nr, st, k0, A2, h, g, ab);
+        }
+    }
+    // The same with zeros for what does not exist, row by row, each from the kept state: slow, but little code.
+    SELINV_DEVINL void real_tile(const C *kept, int nr, uint32_t begins, uint32_t st, int k0, const V (*A2)[KP], V (*g)[KP],
+                                V (*ab)[KP]) const
+    {
+#pragma unroll 1
+        for (int t = nr - 1; t >= 0; --t) {
+            V h[2][KP];
+            load(kept, h);
+#pragma unroll 1
+            for (int s = 0; s < t; ++s) {
+                V a[2][KP];
+                if ((begins >> s) & 1u) states(p.state, sequence(k0, begins, s), h);
+                row<true>(s, A2, h, a);
+            }
+            rows<1, true, true>(t, nr, st, k0, A2, h, g, ab);
         }
     }
     // Bb's and Cb's sums over this warp's channels for rows t .. t + P - 1: a pair of states at a time, from another
@@ -243,15 +303,15 @@ template <class K> constexpr int scan_bwd_blocks = K::SN <= 4 && 3 * (sizeof(Sca
                                                    : 2 * (sizeof(ScanBwdBlock<K>) + 1024) <= 228 * 1024 ? 2
                                                                                                         : 1;
 
-template <class K>
-__global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
-    scan_backward_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ ScanGrads o)
+// A block's work.  States and channels that do not exist stay zero as long as all that is there is finite; with PADDED the
+// call says whether it is not, and with REAL they are kept at zero whatever comes.
+template <class K, bool PADDED, bool REAL>
+SELINV_DEVINL bool scan_backward_block(const ScanArgs &p, const ScanGrads &o, char *smem_raw)
 {
     using T = typename K::T;
     using C = typename K::C;
     using V = typename K::V;
     constexpr int R = SCAN_R, S = SCAN_S, LN = K::LN, LD = K::LD, NP = K::NP, SN = K::SN, KP = K::KP, CW = K::CW, PER = K::PER;
-    extern __shared__ __align__(16) char smem_raw[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     ScanBwdBlock<K> &block = *reinterpret_cast<ScanBwdBlock<K> *>(smem_raw);
     ScanBwdSmem<K> &sm = block.warp[warp];
@@ -346,6 +406,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
     };
     raw_clear_n<SCAN_WARPS * 32>(block.b_raw, n, threadIdx.x);
     raw_clear_n<SCAN_WARPS * 32>(block.c_raw, n, threadIdx.x);
+    C probe = 0;            // of zb; not a number once something is not finite
     __syncthreads();
     int rt = w.r0 + (w.r1 > w.r0 ? (w.r1 - w.r0 - 1) / R * R : 0);
     if (w.r1 > w.r0) fetch(rt);
@@ -400,33 +461,11 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
         }
         __syncthreads();
 
-        V h[2][KP];
         const C *kept = static_cast<const C *>(o.kept) + (w.line * tiles + rt / R) * dn;
-        at.load(kept, h);
-        for (int b = 0; b < R / S - 1 && (b + 1) * S < nr; ++b) {
-            if ((begins >> (b * S)) & ((1u << S) - 1u))
-                at.template skip<true>(b * S, begins, k0, A2, h);
-            else
-                at.template skip<false>(b * S, begins, k0, A2, h);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < KP; ++j) sm.h[b][i * KP + j][lane] = h[i][j];
-        }
-        for (int b = (nr - 1) / S; b >= 0; --b) {
-            if (b > 0) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < KP; ++j) h[i][j] = sm.h[b - 1][i * KP + j][lane];
-            } else {
-                at.load(kept, h);
-            }
-            if ((st >> (b * S)) & ((2u << S) - 1u))
-                at.template rows<true>(b * S, nr, st, k0, A2, h, g, ab);
-            else
-                at.template rows<false>(b * S, nr, st, k0, A2, h, g, ab);
-        }
+        if constexpr (REAL)
+            at.real_tile(kept, nr, begins, st, k0, A2, g, ab);
+        else
+            at.tile(kept, nr, begins, st, k0, A2, g, ab);
         __syncwarp();
         // finish the rows, four of a lane's at a time: all loads, then the arithmetic, then the stores
         constexpr int F = PER < 4 ? PER : 4;
@@ -479,6 +518,14 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
 #pragma unroll
                 for (int i = 0; i < F; ++i)
                     vs[i] = mul2(mul2(ys[i], fma2(sk, xe[i], s[i])), silu_slope2(de[i], sigmoid2(de[i])));
+                if constexpr (PADDED) {
+#pragma unroll
+                    for (int i = 0; i < F; ++i) {
+                        const bool have = nl + LN * (i0 + i) < nr;
+                        if (have && c < w.nch) probe = fma(vs[i].x, (C)0, probe);
+                        if (have && c + 1 < w.nch) probe = fma(vs[i].y, (C)0, probe);
+                    }
+                }
                 put_rows(zb, o.zb.row, rt, nl + LN * i0, nr, w.nch - c, out_wide, vs);
             }
         }
@@ -494,20 +541,53 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
             if (t < nr) part_bc[(int64_t)(rt + t) * p.groups * 2 * NP + j] = v;
         }
     }
-    if (w.nch == 0) return;
-    const int64_t piece = w.line * p.segs + w.seg;
-    at.store(static_cast<C *>(o.part_a) + piece * dn, ab);
-    // lanes that finished the same channels
+    if (w.nch > 0) {
+        const int64_t piece = w.line * p.segs + w.seg;
+        at.store(static_cast<C *>(o.part_a) + piece * dn, ab);
+        // lanes that finished the same channels
 #pragma unroll
-    for (int m = LD; m < 32; m *= 2) {
-        sum_d = add2(sum_d, make2(shfl_xor_(sum_d.x, m), shfl_xor_(sum_d.y, m)));
-        sum_bias = add2(sum_bias, make2(shfl_xor_(sum_bias.x, m), shfl_xor_(sum_bias.y, m)));
+        for (int m = LD; m < 32; m *= 2) {
+            sum_d = add2(sum_d, make2(shfl_xor_(sum_d.x, m), shfl_xor_(sum_d.y, m)));
+            sum_bias = add2(sum_bias, make2(shfl_xor_(sum_bias.x, m), shfl_xor_(sum_bias.y, m)));
+        }
+        if (nl == 0) {
+            C *pd = static_cast<C *>(o.part_d) + piece * p.d + w.c0 + c, *pb = static_cast<C *>(o.part_bias) + piece * p.d + w.c0 + c;
+            if (c < w.nch) pd[0] = sum_d.x, pb[0] = sum_bias.x;
+            if (c + 1 < w.nch) pd[1] = sum_d.y, pb[1] = sum_bias.y;
+        }
     }
-    if (nl == 0) {
-        C *pd = static_cast<C *>(o.part_d) + piece * p.d + w.c0 + c, *pb = static_cast<C *>(o.part_bias) + piece * p.d + w.c0 + c;
-        if (c < w.nch) pd[0] = sum_d.x, pb[0] = sum_bias.x;
-        if (c + 1 < w.nch) pd[1] = sum_d.y, pb[1] = sum_bias.y;
-    }
+    // Every infinity that can make something of what does not exist shows in the block's channels: x and yb' in Db, dt' in
+    // Ab, B and C in dt_biasb, and a product dt' x in Ab or, where no row of its sequence follows, in zb.
+    if (!PADDED) return false;
+    probe = fma(sum_d.x + sum_d.y, (C)0, fma(sum_bias.x + sum_bias.y, (C)0, probe));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < KP; ++j) probe = fma(ab[i][j].x, (C)0, fma(ab[i][j].y, (C)0, probe));
+    return __syncthreads_or(probe != (C)0);
+}
+// PADDED: some states or channels of the blocks do not exist.  Where something is not finite the block then begins again: what
+// tells is in no tile's way, and not in the kernel that has no use for it (4 x 2048 x 4096 in bfloat16, backward: 979 us
+// with 12 states, 955 without any of this; 16 states, all there, 968.  Told apart tile by tile, inside the loop, its
+// registers cost those 60 us.)
+template <class K, bool PADDED>
+__global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
+    scan_backward_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ ScanGrads o)
+{
+    extern __shared__ __align__(16) char smem_raw[];
+    const bool odd = scan_backward_block<K, PADDED, false>(p, o, smem_raw);
+    if constexpr (PADDED)
+        if (odd) scan_backward_block<K, false, true>(p, o, smem_raw);
+}
+template <class K, bool PADDED> cudaError_t scan_backward_start(const ScanArgs &p, const ScanGrads &o, const dim3 &grid, cudaStream_t s)
+{
+    constexpr int bytes = (int)sizeof(ScanBwdBlock<K>);
+    static_assert(bytes <= 227 * 1024, "fits an SM");
+    const cudaError_t e =
+        cudaFuncSetAttribute(scan_backward_kernel<K, PADDED>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    scan_backward_kernel<K, PADDED><<<grid, SCAN_WARPS * 32, bytes, s>>>(p, o);
+    return cudaSuccess;
 }
 
 // What each segment hands to the row before it, from nothing behind it, and the sum of its steps: LN lanes per channel, as
@@ -717,15 +797,13 @@ template <class T, int NP> cudaError_t scan_backward_run(const ScanArgs &p, cons
     const int64_t per = p.d / p.groups, tiles = (per + K::CW - 1) / K::CW;
     const int parts = (int)((tiles + SCAN_WARPS - 1) / SCAN_WARPS);
     const dim3 grid((unsigned)(p.lines * p.segs), (unsigned)(p.groups * parts));
-    constexpr int bytes = (int)sizeof(ScanBwdBlock<K>);
-    static_assert(bytes <= 227 * 1024, "fits an SM");
     if (p.segs > 1) {
         const cudaError_t e = with_lanes<T, NP>(p.ends_lanes, [&](auto k) { return scan_ends_run<decltype(k)>(p, o, s); });
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = cudaFuncSetAttribute(scan_backward_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const bool padded = p.n != NP || per % (K::CW * SCAN_WARPS) != 0;
+    const cudaError_t e = padded ? scan_backward_start<K, true>(p, o, grid, s) : scan_backward_start<K, false>(p, o, grid, s);
     if (e != cudaSuccess) return e;
-    scan_backward_kernel<K><<<grid, SCAN_WARPS * 32, bytes, s>>>(p, o);
     const int64_t bc = (p.lines * p.rows.rows * p.groups * 2 * NP + 255) / 256;
     const int64_t params = (p.d * (p.n + 2) + 31) / 32;
     scan_sums_kernel<T, NP><<<(unsigned)(bc + params), 256, 0, s>>>(p, o, bc, parts);

@@ -42,9 +42,10 @@ template <class K> struct ScanFwdSmem {
     alignas(16) C b[SCAN_R][K::NP], c[SCAN_R][K::NP];
 };
 
-// One row: states on, this lane's part of y.
-template <class K, bool MAIN>
-SELINV_DEVINL typename K::C scan_row(const ScanFwdSmem<K> &sm, int t, int dl, int n0, const typename K::V *A2, typename K::V *h)
+// One row: states on, this lane's part of y.  REAL: keeps those that do not exist (from n on) at zero whatever comes.
+template <class K, bool MAIN, bool REAL>
+SELINV_DEVINL typename K::C scan_row(const ScanFwdSmem<K> &sm, int t, int dl, int n0, int n, const typename K::V *A2,
+                                     typename K::V *h)
 {
     using C = typename K::C;
     using V = typename K::V;
@@ -59,6 +60,7 @@ SELINV_DEVINL typename K::C scan_row(const ScanFwdSmem<K> &sm, int t, int dl, in
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             h[j + i] = fma2(decay2(dt2, A2[j + i]), h[j + i], mul2(u2, b[i]));
+            if (REAL) h[j + i] = real_states(h[j + i], j + i, n);
             if (MAIN) y[i] = fma2(c[i], h[j + i], y[i]);
         }
     }
@@ -141,6 +143,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
         if (MAIN) raw_clear_n<32>(sm.raw[i].c, p.n, lane);
     }
     C total = 0;
+    const bool padded = MAIN && p.n != K::NP;       // some states do not exist
 
     for (int rt = w.r0 - R; rt < w.r1; rt += R) {       // the first time only to fetch: one place in the code that does
         const int at = ((rt - w.r0) / R) & 1;
@@ -152,6 +155,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
         raw_stage_n<32>(sm.b, raw.b, lane);
         if (MAIN) raw_stage_n<32>(sm.c, raw.c, lane);
         const int nr = min(R, w.r1 - rt);
+        bool finite = true;
         {       // all rows' loads before the stores: the chains of one row are long, those of sixteen run side by side
             C v[PER], u[PER];
 #pragma unroll
@@ -169,6 +173,13 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
                 sm.dt[t][dl] = v[i];
                 sm.u[t][dl] = v[i] * u[i];
                 if (!MAIN && t < nr) total += v[i];
+            }
+            if (padded) {       // an infinite step makes this not finite too
+                C probe = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (in && nl + LN * i < nr) probe = fma(v[i] * u[i], (C)0, probe);
+                finite = !__any_sync(FULL_MASK, probe != (C)0);
             }
         }
         __syncwarp();
@@ -188,10 +199,10 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
             }
             const uint32_t later = st >> (t + 1);
             const int te = later ? min(nr, t + __ffs(later)) : nr;
-            for (; t + 4 <= te; t += 4) {       // four rows' loads before their stores
+            for (; finite && t + 4 <= te; t += 4) {     // four rows' loads before their stores
                 C v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = scan_row<K, MAIN>(sm, t + i, dl, n0, A2, h);
+                for (int i = 0; i < 4; ++i) v[i] = scan_row<K, MAIN, false>(sm, t + i, dl, n0, n, A2, h);
                 if (MAIN) {
                     scatter_sum<4, CW, 32>(v, lane);
                     if (LN > 1) __syncwarp();       // a row's sum lands where other lanes read its product
@@ -200,7 +211,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
                 }
             }
             for (; t < te; ++t) {
-                C v[1] = {scan_row<K, MAIN>(sm, t, dl, n0, A2, h)};
+                C v[1] = {scan_row<K, MAIN, MAIN>(sm, t, dl, n0, n, A2, h)};
                 if (MAIN) {
                     scatter_sum<1, CW, 32>(v, lane);
                     if (LN > 1) __syncwarp();

@@ -112,3 +112,68 @@ def test_scan_of_the_widest_layers(cuda_ok, kind, n, groups):
                           ("Bb", b["Bb"][0], d), ("Cb", b["Cb"][0], d)):
         near(k, got, ref[k], mag[k], plain.scan_bound(1, n, width, u))
     assert not b["Ab"].any()
+
+
+def same_infinities(name, got, ref, mag, bound):
+    """Where the definition is finite the result is near it, where it is infinite it is that infinity."""
+    got, finite = got.detach(), np.isfinite(ref) & np.isfinite(mag)
+    assert tuple(got.shape) == ref.shape, name
+    near(name, got[torch.from_numpy(finite).cuda()], ref[finite], mag[finite], bound)
+    inf = np.isinf(ref)
+    bad = host(got)[inf] != ref[inf]
+    assert not bad.any(), (name, int(bad.sum()), np.argwhere(inf)[bad][:4].tolist(), host(got)[inf][bad][:4])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f64"])
+@pytest.mark.parametrize("rows,d,n", [(60, 5, 1), (60, 40, 3), (37, 133, 12), (37, 7, 16), (50, 70, 33), (260, 6, 3)])
+@pytest.mark.parametrize("what", ["x", "yb", "B", "C", "dt", "last"])
+def test_infinities_stay_what_they_are(cuda_ok, kind, rows, d, n, what):
+    """One infinite input of a line, all others positive: what the definition leaves finite or infinite is so in every
+    output, whatever states and channels a tile has that do not exist."""
+    t = TYPES[kind]
+    v, yb, _ = scan_inputs(33, t, (1, rows), d, n, 1)
+    for a in (v["x"], v["B"], v["C"], v["D"], v["z"], yb):
+        a.copy_(0.5 + a.abs())
+    at = rows // 2
+    if what in ("x", "dt"):
+        v[what][0, at, d - 1] = float("inf")
+    elif what == "yb":
+        yb[0, at, d - 1] = float("inf")
+    elif what == "last":        # a state that no row takes up
+        v["x"][0, rows - 1, 0] = float("inf")
+    else:
+        v[what][0, at, 0, n - 1] = float("inf")
+    args, more = [v[k] for k in ("x", "dt", "A", "B", "C")], dict(z=v["z"], dt_bias=v["dt_bias"], softplus=True)
+    r = selinv.selective_scan(*args, v["D"], keep=True, **more)
+    b = selinv.selective_scan_backward(r["kept"], *args, yb, D=v["D"], **more)
+    w = {k: host(a) if k in ("A", "D", "dt_bias", "state") else host(a)[0] for k, a in v.items()}
+    with np.errstate(all="ignore"):
+        ref, mag = (plain.scan(**w, softplus=True, yb=host(yb)[0], mag=m) for m in (False, True))
+    u = unit(arith(t))
+    bound, sums = plain.scan_bound(rows, n, d, u), plain.scan_bound(rows, n, d + rows, u)
+    same_infinities("y", r["y"][0], ref["y"], mag["y"], bound)
+    same_infinities("state", r["state"][0], ref["state"], mag["state"], bound)
+    for k in ("xb", "dtb", "Bb", "Cb", "zb"):
+        same_infinities(k, b[k][0], ref[k], mag[k], bound)
+    for k in ("Ab", "Db", "dt_biasb"):
+        same_infinities(k, b[k], ref[k], mag[k], sums)
+
+
+@pytest.mark.parametrize("n", [3, 12])
+def test_infinities_in_prompts_and_tokens(cuda_ok, n):
+    """A prompt and single tokens agree on what becomes of an infinite input."""
+    v, _, _ = scan_inputs(34, torch.float32, (40, 1), 9, n, 1)
+    for k in ("B", "C", "D", "z"):
+        v[k].abs_()
+    v["x"][7, 0, 4] = float("inf")
+    v["x"][20, 0, 6] = float("-inf")
+    more = dict(dt_bias=v["dt_bias"], softplus=True)
+    line = {k: v[k].transpose(0, 1) for k in ("x", "dt", "B", "C", "z")}
+    r = selinv.selective_scan(line["x"], line["dt"], v["A"], line["B"], line["C"], v["D"], z=line["z"], **more)
+    cache = torch.zeros(1, 9, n, device="cuda")
+    for i in range(40):
+        y = selinv.selective_scan_step(cache, v["x"][i], v["dt"][i], v["A"], v["B"][i], v["C"][i], v["D"], z=v["z"][i], **more)
+        p = r["y"][:, i]
+        assert torch.equal(torch.isinf(y), torch.isinf(p)) and not torch.isnan(p).any(), i
+        assert torch.allclose(p, y, rtol=1e-4, atol=1e-5)
+    assert torch.allclose(cache, r["state"], rtol=1e-4, atol=1e-5) and torch.isinf(cache).sum() == 2 * n
