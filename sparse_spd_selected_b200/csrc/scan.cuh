@@ -246,7 +246,8 @@ template <int N, class V> SELINV_DEVINL void zero_states(V *v)
 // What the segments s, s + by, ... before `to` hand on to N states of one channel (own: their place in a [d, n] array):
 // the first one's own, decayed by each later one's sum of steps and joined to that one's own.  The decays of a whole
 // segment are taken in two halves of at most 2^127 (2^1023) each: steps that let a state grow (dt' A > 0) may leave
-// that range although the state does not, and nothing times that is nothing.
+// that range although the state does not, and nothing times that is nothing.  Nor is a half below 2^-126 (2^-1022): what
+// that leaves of a finite state is nothing to it, but zero times an infinite one is not a number.
 template <int N, class C>
 SELINV_DEVINL void scan_join(const ScanArgs &p, int64_t line, int s, int to, int by, int64_t channel, int64_t own, int m, bool in,
                              const typename Two<C>::V *A2, typename Two<C>::V *h)
@@ -259,10 +260,10 @@ SELINV_DEVINL void scan_join(const ScanArgs &p, int64_t line, int s, int to, int
     for (s += by; s != to; s += by) {
         V e[N / 2];
         load_states<N>(ends + s * dn, m, in, e);
-        const C t = in ? sums[s * p.d] / 2 : (C)0, most = sizeof(C) == 4 ? 127 : 1023;
+        const C t = in ? sums[s * p.d] / 2 : (C)0, most = sizeof(C) == 4 ? 127 : 1023, least = 1 - most;
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
-            const V a = exp2_2(make2(fmin(t * A2[j].x, most), fmin(t * A2[j].y, most)));
+            const V a = exp2_2(make2(fmax(fmin(t * A2[j].x, most), least), fmax(fmin(t * A2[j].y, most), least)));
             h[j] = fma2(a, mul2(a, h[j]), e[j]);
         }
     }

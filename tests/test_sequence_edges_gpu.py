@@ -177,3 +177,34 @@ def test_infinities_in_prompts_and_tokens(cuda_ok, n):
         assert torch.equal(torch.isinf(y), torch.isinf(p)) and not torch.isnan(p).any(), i
         assert torch.allclose(p, y, rtol=1e-4, atol=1e-5)
     assert torch.allclose(cache, r["state"], rtol=1e-4, atol=1e-5) and torch.isinf(cache).sum() == 2 * n
+
+
+@pytest.mark.parametrize("kind", ["f32", "f64"])
+def test_infinite_states_outlive_their_decay(cuda_ok, kind):
+    """A line cut into segments, each of which decays a state by more than the type's range: an infinite state, and an
+    infinite cotangent of one, stay infinite over all of them, as row after row, and other channels' vanish."""
+    t, rows, d, n = TYPES[kind], 600, 6, 4
+    step = 3.0 if kind == "f32" else 30.0
+    v, yb, stateb = scan_inputs(35, t, (1, rows), d, n, 1, softplus=False, bias=False, skip=False, states=(1,))
+    v["A"].fill_(-2)
+    v["dt"].fill_(step)
+    for a in (v["x"], v["B"], v["C"], v["z"], yb):
+        a.copy_(0.5 + a.abs())
+    v["x"][0, 5, 1] = float("inf")
+    stateb[0, 3] = float("inf")
+    args = [v[k] for k in ("x", "dt", "A", "B", "C")]
+    assert selinv.lib().selinv_selective_scan_workspace_size(
+        selinv._scan_inputs(*args, None, v["z"], None, False, v["state"], None)[0]) > 0      # it is cut
+    r = selinv.selective_scan(*args, z=v["z"], state=v["state"], keep=True)
+    b = selinv.selective_scan_backward(r["kept"], *args, yb, z=v["z"], state=v["state"], stateb=stateb)
+    w = {k: host(a) if a is None or k == "A" else host(a)[0] for k, a in v.items()}
+    with np.errstate(all="ignore"):
+        ref, mag = (plain.scan(**w, yb=host(yb)[0], stateb=host(stateb)[0], mag=m) for m in (False, True))
+    assert np.isinf(ref["state"][1]).all() and np.isinf(ref["stateb"][3]).all() and np.isfinite(ref["state"][0]).all()
+    # the decays' arguments are 2 steps a row: an error of three units each is that many units of what is left of a state
+    u = unit(arith(t))
+    bound = plain.scan_bound(1, n, d, u) + 8 * 2 * step * u
+    for k in ("y", "xb", "zb"):
+        same_infinities(k, r[k][0] if k == "y" else b[k][0], ref[k], mag[k], bound)
+    same_infinities("state", r["state"][0], ref["state"], mag["state"], bound)
+    same_infinities("stateb", b["stateb"][0], ref["stateb"], mag["stateb"], bound)
