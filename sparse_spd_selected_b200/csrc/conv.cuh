@@ -293,22 +293,32 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_backward_kernel(const __gri
                     }
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
-                        const bool ours = t + i < w.r1;
                         const int m = t + i - (K - 1);
                         V v[EP];
 #pragma unroll
                         for (int e = 0; e < EP; ++e) {
                             ring[K - 1 + i][e] = g[i][e];
-                            if (!ours) g[i][e] = none[e];       // summed by the next chunk
-                            bsum[e] = add2(bsum[e], g[i][e]);
                             v[e] = mul2(wt[K - 1][e], ring[i][e]);
 #pragma unroll
-                            for (int j = 0; j < K; ++j) {
-                                wsum[j][e] = fma2(g[i][e], win[i + j][e], wsum[j][e]);
-                                if (j) v[e] = fma2(wt[K - 1 - j][e], ring[i + j][e], v[e]);
-                            }
+                            for (int j = 1; j < K; ++j) v[e] = fma2(wt[K - 1 - j][e], ring[i + j][e], v[e]);
                         }
                         if (m >= max(m0, start) && m < m1) down_row(xb + (int64_t)m * p.xb.row, E, p.xb.wide, v);
+                    }
+                    const auto sum = [&](int i) {
+#pragma unroll
+                        for (int e = 0; e < EP; ++e) {
+                            bsum[e] = add2(bsum[e], g[i][e]);
+#pragma unroll
+                            for (int j = 0; j < K; ++j) wsum[j][e] = fma2(g[i][e], win[i + j][e], wsum[j][e]);
+                        }
+                    };
+                    if (t + U <= w.r1) {
+#pragma unroll
+                        for (int i = 0; i < U; ++i) sum(i);
+                    } else {            // rows from r1 on are the next chunk's to sum
+#pragma unroll
+                        for (int i = 0; i < U; ++i)
+                            if (t + i < w.r1) sum(i);
                     }
                     conv_shift<K, U, EP>(win);
                     conv_shift<K, U, EP>(ring);

@@ -208,3 +208,24 @@ def test_infinite_states_outlive_their_decay(cuda_ok, kind):
         same_infinities(k, r[k][0] if k == "y" else b[k][0], ref[k], mag[k], bound)
     same_infinities("state", r["state"][0], ref["state"], mag["state"], bound)
     same_infinities("stateb", b["stateb"][0], ref["stateb"], mag["stateb"], bound)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f64"])
+@pytest.mark.parametrize("k", [2, 4, 7])
+def test_conv_infinities_next_to_a_chunks_end(cuda_ok, kind, k):
+    """Each channel has one infinite input, in a row of its own: the chunk before it, which reads it for its last rows'
+    cotangents, does not make something else of weightb."""
+    t, rows = TYPES[kind], 200
+    g = np.random.default_rng(36)
+    x, yb = (dev(0.5 + g.random((1, rows, rows)), t) for _ in range(2))
+    weight = dev(0.5 + g.random((rows, k)), t)
+    x[0].diagonal().fill_(float("inf"))
+    r = selinv.causal_conv(x, weight)
+    b = selinv.causal_conv_backward(x, weight, yb)
+    with np.errstate(all="ignore"):
+        ref, mag = (plain.conv(host(x)[0], host(weight), yb=host(yb)[0], mag=m) for m in (False, True))
+    u = unit(arith(t))
+    same_infinities("y", r["y"][0], ref["y"], mag["y"], plain.conv_bound(0, k, u))
+    same_infinities("xb", b["xb"][0], ref["xb"], mag["xb"], plain.conv_bound(0, k, u))
+    for key in ("weightb", "biasb"):
+        same_infinities(key, b[key], ref[key], mag[key], plain.conv_bound(rows, k, u))
