@@ -437,7 +437,7 @@ SELINV_DEVINL bool scan_backward_block(const ScanArgs &p, const ScanGrads &o, ch
             }
             if (p.softplus) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) a[i] = softplus2(a[i]);
+                for (int i = 0; i < PER; ++i) a[i] = make2(softplus_of<T>(a[i].x), softplus_of<T>(a[i].y));
             }
             if (z) {
 #pragma unroll
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
             }
             if (p.softplus) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) a[i] = softplus_(a[i]);
+                for (int i = 0; i < PER; ++i) a[i] = softplus_of<T>(a[i]);
             }
             if (z) {
 #pragma unroll

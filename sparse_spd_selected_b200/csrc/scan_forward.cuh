@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
             }
             if (p.softplus) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) v[i] = softplus_(v[i]);
+                for (int i = 0; i < PER; ++i) v[i] = softplus_of<T>(v[i]);
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i) {

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(STEP_THREADS) scan_step_kernel(const __grid_co
     const int per = p.groups == 1 ? d : d / p.groups;
     C b[4], cc[4], v[LN];
     int group = -1;
-    if (p.softplus) dt = softplus_(dt);
+    if (p.softplus) dt = softplus_of<T>(dt);
     const C ux = dt * x, d2 = dt * log2e<C>();
 #pragma unroll
     for (int u0 = 0; u0 < LN; u0 += U) {

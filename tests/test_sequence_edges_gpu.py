@@ -229,3 +229,125 @@ def test_conv_infinities_next_to_a_chunks_end(cuda_ok, kind, k):
     same_infinities("xb", b["xb"][0], ref["xb"], mag["xb"], plain.conv_bound(0, k, u))
     for key in ("weightb", "biasb"):
         same_infinities(key, b[key], ref[key], mag[key], plain.conv_bound(rows, k, u))
+
+
+def relative(got, ref):
+    """Errors in units of float's rounding (2^-24), relative to each value."""
+    return np.abs(host(got).reshape(ref.shape) - ref) / np.abs(ref) / 2.0 ** -24
+
+
+def spread_out(lo, hi, count, seed):
+    """Values over a range, and close to zero and to the whole numbers within it."""
+    g = np.random.default_rng(seed)
+    v = np.concatenate([g.uniform(lo, hi, count), g.uniform(max(lo, -1.0), min(hi, 1.0), count // 4),
+                        np.arange(np.ceil(lo), np.floor(hi) + 1), [2.0 ** -i for i in range(40) if lo <= 2.0 ** -i <= hi],
+                        [-2.0 ** -i for i in range(40) if lo <= -2.0 ** -i <= hi]])
+    return v.astype(np.float32)
+
+
+def row_of(dt, z=None, A=None, state=None, x=1.0, D=None):
+    """One row with a channel per value of dt, one state, B = C = 1: forward with its kept states, and the arguments."""
+    d = dt.numel()
+    one = torch.ones(1, 1, 1, device="cuda")
+    xs = torch.full((1, d), x, device="cuda")
+    A = torch.zeros(d, 1, device="cuda") if A is None else A
+    args = (xs, dt[None], A, one, one)
+    return args, dict(z=None if z is None else z[None], D=D, state=state)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_steps_from_16_bits_far_from_zero(cuda_ok, kind):
+    """Steps that the float biases carry far from zero: 1.3 units of |x| more, for the argument's roundings."""
+    v = spread_out(-86.5, 86.5, 40000, 1)
+    ref = np.logaddexp(v.astype(np.float64), 0)
+    t = TYPES[kind]
+    one, x = torch.ones(1, 1, 1, dtype=t, device="cuda"), torch.ones(1, v.size, dtype=t, device="cuda")
+    args = (x, torch.zeros_like(x), torch.zeros(v.size, 1, device="cuda"), one, one)
+    more = dict(dt_bias=torch.from_numpy(v).cuda(), softplus=True)
+    cache = torch.zeros(1, v.size, 1, device="cuda")
+    selinv.selective_scan_step(cache, *args, **more)
+    for name, got in (("state", selinv.selective_scan(*args, **more)["state"]), ("cache", cache)):
+        assert (relative(got, ref) <= 12 + 1.3 * np.abs(v)).all(), name
+
+
+def test_steps_far_from_zero(cuda_ok):
+    """softplus over its whole range, to a few units relative to the step itself, in every kernel that forms it.
+
+    With A = 0, x = B = 1 and no state the state is the step, with C = 1 and yb = 1 so is xb.  Its roundings: the power of
+    two 4 units, the correction of its argument 1, the polynomial 1 for its fit and 3 for its arithmetic, the sum 1, and
+    the kernels' products 2."""
+    v = spread_out(-86.5, 86.5, 40000, 1)
+    ref = np.logaddexp(v.astype(np.float64), 0)
+    dt = torch.from_numpy(v).cuda()
+    args, more = row_of(dt)
+    r = selinv.selective_scan(*args, softplus=True, keep=True)
+    b = selinv.selective_scan_backward(r["kept"], *args, torch.ones_like(args[0]), softplus=True)
+    cache = torch.zeros(1, v.size, 1, device="cuda")
+    selinv.selective_scan_step(cache, *args, softplus=True)
+    for name, got in (("state", r["state"]), ("xb", b["xb"]), ("cache", cache)):
+        off = relative(got, ref)
+        assert off.max() <= 12, (name, off.max(), v[off.argmax()])
+    # dt's cotangent is the sigmoid: the argument of its power is off by 1.3 units of itself, so e^-x by 1.3 |x|; 4 for the
+    # power, 1 for the sum, 2 for the reciprocal and 1 for the product
+    off = relative(b["dtb"], 1 / (1 + np.exp(-v.astype(np.float64))))
+    assert (off <= 8 + 1.3 * np.abs(v)).all(), (off - 1.3 * np.abs(v)).max()
+
+
+def test_gates_far_from_zero(cuda_ok):
+    """silu over its whole range: y of a state that is not read and D = x = 1 in the scan, of a single tap in the
+    convolution.  The sigmoid's roundings are those above, with 2 more products."""
+    v = spread_out(-86.5, 100.0, 40000, 2)
+    w = v.astype(np.float64)
+    keep = w != 0
+    ref = w / (1 + np.exp(-w))
+    bound = 10 + 1.3 * np.abs(w)
+    z = torch.from_numpy(v).cuda()
+    zero = torch.zeros_like(z)
+    args, more = row_of(zero, z=z, D=torch.ones_like(z))
+    y = selinv.selective_scan(*args, **more)["y"]
+    token = selinv.selective_scan_step(torch.zeros(1, v.size, 1, device="cuda"), *args, more["D"], z=more["z"])
+    taps = torch.tensor([[0.0, 1.0]], device="cuda").expand(v.size, 2).contiguous()
+    conv = selinv.causal_conv(z[None], taps, silu=True)["y"]
+    tap = selinv.causal_conv_step(torch.zeros(1, 1, v.size, device="cuda"), z[None], taps, silu=True)
+    for name, got in (("scan", y), ("scan step", token), ("conv", conv), ("conv step", tap)):
+        off = relative(got[0].cpu()[keep], ref[keep])
+        assert (off <= bound[keep]).all(), (name, (off - bound[keep]).max())
+        assert not host(got)[0][~keep].any(), name
+    assert torch.equal(selinv.causal_conv(torch.full((1, 8), -1e4, device="cuda"), taps[:8], silu=True)["y"],
+                       torch.zeros(1, 8, device="cuda"))
+
+
+def test_decays_far_from_zero(cuda_ok):
+    """exp(dt' A) over its whole range: of a state of one with x = 0 it is what is left.  The argument is off by 2.3 units of
+    itself (A log2 e, the product, log2 e's own rounding), the power by 4, the state's product by 1, 1 to spare."""
+    v = spread_out(-86.0, 0.0, 40000, 3)
+    v = v[v < 0]
+    dt, A = torch.from_numpy(-v).cuda(), -torch.ones(v.size, 1, device="cuda")
+    state = torch.ones(v.size, 1, device="cuda")
+    ref = np.exp(v.astype(np.float64))
+    args, more = row_of(dt, A=A, x=0.0, state=state)
+    r = selinv.selective_scan(*args, **more, keep=True)
+    b = selinv.selective_scan_backward(r["kept"], *args, torch.ones_like(args[0]), state=state)
+    cache = state.clone()[None]
+    selinv.selective_scan_step(cache, *args)
+    for name, got in (("state", r["state"]), ("stateb", b["stateb"]), ("cache", cache)):
+        off = relative(got, ref)
+        assert (off <= 6 + 2.3 * np.abs(v)).all(), (name, (off - 2.3 * np.abs(v)).max())
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f64"])
+@pytest.mark.parametrize("rows,d", [(700, 8), (40, 3000)])
+def test_rows_without_a_step_leave_the_state(cuda_ok, kind, rows, d):
+    """dt' = 0, as in a padded batch: the state stays bit for bit what it is, and so does its cotangent on the way back."""
+    t, n = TYPES[kind], 5
+    v, yb, stateb = scan_inputs(37, t, (1, rows), d, n, 1, softplus=False, bias=False, states=(1,))
+    v["dt"].zero_()
+    yb.zero_()
+    args = [v[k] for k in ("x", "dt", "A", "B", "C")]
+    r = selinv.selective_scan(*args, v["D"], z=v["z"], state=v["state"], keep=True)
+    b = selinv.selective_scan_backward(r["kept"], *args, yb, D=v["D"], z=v["z"], state=v["state"], stateb=stateb)
+    assert torch.equal(r["state"], v["state"]) and torch.equal(b["stateb"], stateb)
+    assert not b["xb"].any() and not b["Ab"].any() and not b["Bb"].any()
+    cache = v["state"].clone()
+    selinv.selective_scan_step(cache, v["x"][:, 0], v["dt"][:, 0], v["A"], v["B"][:, 0], v["C"][:, 0])
+    assert torch.equal(cache, v["state"])
