@@ -1180,6 +1180,18 @@ def _dense_output(out, key, shape, dtype, device, inputs):
     return t
 
 
+def _scratch(nbytes, device, workspace, others):
+    """A workspace of nbytes, or the caller's where one is given: bytes in one piece on `device`, apart from the call's
+    inputs and outputs (`others`)."""
+    if workspace is not None and nbytes:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != device:
+            raise ValueError(f"workspace must be a tensor on {device}")
+        if not workspace.is_contiguous() or workspace.data_ptr() % 16:
+            raise ValueError("workspace must be contiguous and begin on 16 bytes")
+        _apart("workspace", workspace.view(-1).view(torch.uint8), others)
+    return _workspace(nbytes, device, workspace)
+
+
 def _conv_inputs(x, weight, bias, silu, state, plan):
     code, dt, dev = _element_code("x", x), x.dtype, x.device
     lines, rows, sequences, live, table, lead = _rows_of("x", x, plan)
@@ -1224,14 +1236,15 @@ def causal_conv_backward(x, weight, yb, *, bias=None, stateb=None, silu=False, s
     packed, states, d, k = _conv_inputs(x, weight, bias, silu, state, plan)
     dt, dev, ct = x.dtype, x.device, _arith(x.dtype)
     _like("yb", yb, dt, dev, x.shape, contiguous=False)
-    given = [("x", x), ("weight", weight), ("bias", bias), ("state", state), ("yb", yb), ("stateb", stateb)] if out else []
+    given = [("x", x), ("weight", weight), ("bias", bias), ("state", state), ("yb", yb), ("stateb", stateb)] \
+        if out or workspace is not None else []
     xb = _output(out, "xb", x.shape, dt, dev, plan, given)
     weightb = _dense_output(out, "weightb", (d, k), ct, dev, given)
     biasb = _dense_output(out, "biasb", (d,), ct, dev, given)
     new = _dense_output(out, "stateb", states, dt, dev, given) if state is not None else None
     L = lib()
     nbytes = L.selinv_causal_conv_backward_workspace_size(packed)
-    ws = _workspace(nbytes, dev, workspace)
+    ws = _scratch(nbytes, dev, workspace, given)
     grads = _CONV_GRADS.pack(*_view("yb", yb, 1), _like("stateb", stateb, dt, dev, states),
                              *_view("xb", xb, 1, out is not None), weightb.data_ptr(), biasb.data_ptr(),
                              0 if new is None else new.data_ptr())
@@ -1395,10 +1408,11 @@ def selective_scan(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=Fal
     Returns a dict with y, state (the final states, if want_state) and kept
     (what selective_scan_backward needs, if keep).  ``out`` may hold
     preallocated y and state (not overlapping the inputs or
-    each other)."""
+    each other), and ``workspace`` be a contiguous tensor of the C query's
+    size, apart from all of them."""
     packed, states, d, n, groups, _ = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, state, plan)
     dev, ct = x.device, _arith(x.dtype)
-    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state) if out else []
+    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state) if out or workspace is not None else []
     y = _output(out, "y", x.shape, x.dtype, dev, plan, given)
     new = _dense_output(out, "state", states, ct, dev, given) if want_state else None
     L = lib()
@@ -1406,7 +1420,7 @@ def selective_scan(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=Fal
     if keep:
         kept = torch.empty(L.selinv_selective_scan_kept_size(packed) // ct.itemsize, dtype=ct, device=dev)
     nbytes = L.selinv_selective_scan_workspace_size(packed)
-    ws = _workspace(nbytes, dev, workspace)
+    ws = _scratch(nbytes, dev, workspace, given)
     _check(L.selinv_selective_scan(packed, _VIEW.pack(*_view("y", y, 1, out is not None)),
                                    0 if new is None else new.data_ptr(), 0 if kept is None else kept.data_ptr(),
                                    0 if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev)), "selinv_selective_scan")
@@ -1424,13 +1438,14 @@ def selective_scan_backward(kept, x, dt, A, B, C, yb, *, D=None, stateb=None, z=
     L = lib()
     _like("kept", kept, ct, dev, (L.selinv_selective_scan_kept_size(packed) // ct.itemsize,))
     _like("yb", yb, ty, dev, x.shape, False)
-    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state, ("kept", kept), ("yb", yb), ("stateb", stateb)) if out else []
+    given = _scan_given(x, dt, A, B, C, D, z, dt_bias, state, ("kept", kept), ("yb", yb), ("stateb", stateb)) \
+        if out or workspace is not None else []
     new = {k: _output(out, k, s, ty, dev, plan, given) for k, s in (("xb", x.shape), ("dtb", x.shape), ("Bb", bc), ("Cb", bc))}
     new["zb"] = _output(out, "zb", x.shape, ty, dev, plan, given) if z is not None else None
     for key, ref, shape in (("Ab", A, (d, n)), ("Db", D, (d,)), ("dt_biasb", dt_bias, (d,)), ("stateb", state, states)):
         new[key] = _dense_output(out, key, shape, ct, dev, given) if ref is not None else None
     nbytes = L.selinv_selective_scan_backward_workspace_size(packed)
-    ws = _workspace(nbytes, dev, workspace)
+    ws = _scratch(nbytes, dev, workspace, given)
     own = out is not None
     Bb, Cb, zb = new["Bb"], new["Cb"], new["zb"]
     grads = _SCAN_GRADS.pack(kept.data_ptr(), *_view("yb", yb, 1), _like("stateb", stateb, ct, dev, states),

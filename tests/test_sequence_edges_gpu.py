@@ -351,3 +351,33 @@ def test_rows_without_a_step_leave_the_state(cuda_ok, kind, rows, d):
     cache = v["state"].clone()
     selinv.selective_scan_step(cache, v["x"][:, 0], v["dt"][:, 0], v["A"], v["B"][:, 0], v["C"][:, 0])
     assert torch.equal(cache, v["state"])
+
+
+def test_workspaces_that_cannot_be_are_refused(cuda_ok):
+    """On the host, in pieces, off 16 bytes, or shared with an input or an output: refused before anything is launched."""
+    v, yb, _ = scan_inputs(38, torch.float32, (1, 600), 16, 16, 1)
+    args = [v[k] for k in ("x", "dt", "A", "B", "C")]
+    r = selinv.selective_scan(*args, keep=True)
+    size = 1 << 22
+    ws = torch.zeros(2 * size, dtype=torch.uint8, device="cuda")
+    inner = ws[:600 * 16 * 4].view(torch.float32).view(1, 600, 16)
+    w = torch.ones(16, 4, device="cuda")
+    forward = lambda **k: selinv.selective_scan(*args, **k)                                     # noqa: E731
+    backward = lambda **k: selinv.selective_scan_backward(r["kept"], *args, yb, **k)            # noqa: E731
+    conv = lambda **k: selinv.causal_conv_backward(v["x"], w, yb, **k)                          # noqa: E731
+    for call, key in ((forward, "y"), (backward, "xb"), (conv, "xb")):
+        for bad in (torch.zeros(size, dtype=torch.uint8), ws[::2], ws[4:size], "here", np.zeros(size, np.uint8)):
+            with pytest.raises(ValueError):
+                call(workspace=bad)
+        with pytest.raises(ValueError):
+            call(workspace=ws, out={key: inner})
+        call(workspace=ws[size:], out={key: inner})
+        call(workspace=ws.view(torch.float64))
+    whole = torch.zeros(size + 600 * 16, device="cuda")
+    x = whole[-600 * 16:].view(1, 600, 16)
+    for call in (lambda k: selinv.selective_scan(x, *args[1:], workspace=k),
+                 lambda k: selinv.selective_scan_backward(r["kept"], x, *args[1:], yb, workspace=k),
+                 lambda k: selinv.causal_conv_backward(x, w, yb, workspace=k)):
+        with pytest.raises(ValueError):
+            call(whole)
+        call(whole[:size])
