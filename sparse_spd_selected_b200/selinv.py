@@ -1022,6 +1022,8 @@ def _like(name, t, dtype, device, shape, contiguous=True):
 def _view(name, t, inner, output=False):
     """(address, stride between lines, stride between rows) of a tensor [..., rows, *inner dims]: its last dimension
     contiguous, its leading dimensions one even stride apart."""
+    if t is None:
+        raise ValueError(f"{name} must be a tensor")
     st, sh = t.stride(), t.shape
     at = len(sh) - 1 - inner
     if at == 0 and st[-1] == 1 and not output:
@@ -1146,6 +1148,8 @@ def _rows_of(name, x, plan, inner=1):
         for n in lead:
             lines *= n
         return lines, rows, 0, 0, 0, tuple(lead)
+    if not isinstance(plan, SequencePlan):
+        raise ValueError("plan must be a SequencePlan")
     if lead:
         raise ValueError(f"with a plan {name} must be [rows, d]")
     if plan.rows > rows:
@@ -1308,6 +1312,8 @@ def _step_slots(cache, shape, batch, index, cache_out, check, dev):
     slots = cache.shape[0]
     if cache_out is None:
         cache_out = cache
+    elif not isinstance(cache_out, torch.Tensor):
+        raise ValueError(f"cache_out must be a tensor on {dev}")
     else:
         gap = cache_out.data_ptr() - cache.data_ptr()       # both contiguous, of one shape and type (checked below)
         if gap and -cache_out.nbytes < gap < cache.nbytes:

@@ -381,3 +381,30 @@ def test_workspaces_that_cannot_be_are_refused(cuda_ok):
         with pytest.raises(ValueError):
             call(whole)
         call(whole[:size])
+
+
+def test_missing_tensors_are_refused(cuda_ok):
+    """What a call cannot do without, given as None or as something else: a ValueError that names it."""
+    v, yb, _ = scan_inputs(39, torch.float32, (2, 6), 8, 4, 2, states=(2,))
+    full = {k: v[k] for k in ("x", "dt", "A", "B", "C")}
+    kept = selinv.selective_scan(*full.values(), keep=True)["kept"]
+    token = {k: a if k == "A" else a[:, 0] for k, a in full.items()}
+    w, x = torch.ones(8, 4, device="cuda"), v["x"]
+    cache = torch.zeros(2, 3, 8, device="cuda")
+    for bad in (None, [1.0], np.zeros(3)):
+        for k in full:
+            for call in (lambda a: selinv.selective_scan(*a), lambda a: selinv.selective_scan_backward(kept, *a, yb)):
+                with pytest.raises(ValueError, match=f"^{k} "):
+                    call(list({**full, k: bad}.values()))
+            with pytest.raises(ValueError, match=f"{k} must|{k} \\["):
+                selinv.selective_scan_step(v["state"].clone(), *{**token, k: bad}.values())
+        for call in (lambda: selinv.selective_scan_backward(kept, *full.values(), bad), lambda: selinv.causal_conv(bad, w),
+                     lambda: selinv.selective_scan_backward(bad, *full.values(), yb), lambda: selinv.causal_conv(x, bad),
+                     lambda: selinv.causal_conv_backward(x, w, bad), lambda: selinv.causal_conv_step(cache, bad, w),
+                     lambda: selinv.causal_conv_step(bad, x[:, 0], w), lambda: selinv.causal_conv_step(cache, x[:, 0], bad)):
+            with pytest.raises(ValueError):
+                call()
+    with pytest.raises(ValueError):
+        selinv.causal_conv_step(cache, x[:, 0], w, cache_out=[1.0])
+    with pytest.raises(ValueError):
+        selinv.causal_conv(x[0], w, plan=[4, 2])
