@@ -572,8 +572,9 @@ selinv_status selinv_selective_scan_backward(const selinv_scan_inputs *a, const 
  * Selective scan for single tokens: row r of [batch, ...] continues the state
  * cache[index[r]] (cache [slots, d, n]; index NULL: slot r), which goes to the
  * same slot of cache_out (the cache itself, or another array of its shape; the
- * slots that no row names are not written).  index[r] = -1 skips the row: its y
- * is zero.  A slot outside the cache, or one that an earlier row names too, is
+ * slots that no row names are not written); no other array may overlap
+ * cache_out (SELINV_ERR_INVALID_ARG).  index[r] = -1 skips the row: its y is
+ * zero.  A slot outside the cache, or one that an earlier row names too, is
  * skipped the same way and reported: info[r] (may be NULL) is -1, or 0 (outside)
  * or 1 (named twice).
  */

@@ -71,6 +71,18 @@ selinv_status rows_check(int64_t lines, int64_t rows, const int64_t *table, int6
     return rows > MAX_ROWS ? SELINV_ERR_UNSUPPORTED : SELINV_OK;
 }
 
+// The cache that a step writes, n elements of the given size: its rows are done in no order, so nothing else lies in it.
+struct Written {
+    uintptr_t lo, hi;
+    Written(const void *p, int64_t n, size_t size) : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + n * size) {}
+    // Whether n elements at p lie beside it (or p is null).
+    bool beside(const void *p, int64_t n, size_t size) const
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        return !p || at >= hi || at + n * size <= lo;
+    }
+};
+
 // ---- selective scan ----------------------------------------------------------
 
 selinv_status scan_check(const selinv_scan_inputs &a)
@@ -353,6 +365,17 @@ selinv_status selinv_selective_scan_step(const selinv_scan_step *a, void *stream
     if (a->x_row < 0 || a->dt_row < 0 || a->z_row < 0 || a->B_row < 0 || a->C_row < 0 || a->B_group < 0 || a->C_group < 0 ||
         a->y_row < 0)
         return SELINV_ERR_INVALID_ARG;
+    const int64_t last = a->batch - 1, states = a->slots * a->d * a->n;
+    const Written w(a->cache_out, states, cs);
+    const auto row = [&](const void *v, int64_t stride) { return w.beside(v, last * stride + a->d, es); };
+    const auto groups = [&](const void *v, int64_t stride, int64_t group) {
+        return w.beside(v, last * stride + (a->groups - 1) * group + a->n, es);
+    };
+    if (!row(a->x, a->x_row) || !row(a->dt, a->dt_row) || !row(a->z, a->z_row) || !row(a->y, a->y_row) ||
+        !groups(a->B, a->B_row, a->B_group) || !groups(a->C, a->C_row, a->C_group) || !w.beside(a->A, a->d * a->n, cs) ||
+        !w.beside(a->D, a->d, cs) || !w.beside(a->dt_bias, a->d, cs) || !w.beside(a->index, a->batch, 4) ||
+        !w.beside(a->info, a->batch, 4) || (a->cache != a->cache_out && !w.beside(a->cache, states, cs)))
+        return SELINV_ERR_INVALID_ARG;
     if (a->batch * div_up(a->d, 128) > MAX_GRID_X) return SELINV_ERR_UNSUPPORTED;
     ScanStepArgs p{};
     p.batch = a->batch, p.d = a->d, p.slots = a->slots, p.n = (int)a->n, p.groups = (int)a->groups;
@@ -432,6 +455,12 @@ selinv_status selinv_causal_conv_step(const selinv_conv_step *a, void *stream)
     for (const void *p : elems)
         if (!p || !aligned(p, es)) return SELINV_ERR_INVALID_ARG;
     if (!aligned(a->bias, es) || !aligned(a->index, 4) || !aligned(a->info, 4) || a->x_row < 0 || a->y_row < 0)
+        return SELINV_ERR_INVALID_ARG;
+    const int64_t last = a->batch - 1, states = a->slots * (a->k - 1) * a->d;
+    const Written w(a->cache_out, states, es);
+    if (!w.beside(a->x, last * a->x_row + a->d, es) || !w.beside(a->y, last * a->y_row + a->d, es) ||
+        !w.beside(a->weight, a->d * a->k, es) || !w.beside(a->bias, a->d, es) || !w.beside(a->index, a->batch, 4) ||
+        !w.beside(a->info, a->batch, 4) || (a->cache != a->cache_out && !w.beside(a->cache, states, es)))
         return SELINV_ERR_INVALID_ARG;
     if (a->batch * div_up(a->d, 128) > MAX_GRID_X) return SELINV_ERR_UNSUPPORTED;
     ConvStepArgs p{};

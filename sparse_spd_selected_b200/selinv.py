@@ -1331,6 +1331,16 @@ def _step_slots(cache, shape, batch, index, cache_out, check, dev):
     return slots, cache_out, at, info
 
 
+def _off_cache(cache_out, others):
+    """Names the first of a step's inputs that shares memory with the cache that is written."""
+    lo, hi = _span(cache_out)
+    for name, t in others:
+        if t is not None:
+            a, b = _span(t)
+            if a < hi and lo < b:
+                raise ValueError(f"{name} must not overlap the cache that is written")
+
+
 def _raise_on_slots(info):
     if info is not None:
         host = info.cpu()
@@ -1341,8 +1351,8 @@ def _raise_on_slots(info):
 @_placed("cache")
 def causal_conv_step(cache, x, weight, bias=None, *, silu=False, index=None, cache_out=None, check=True, out=None):
     """causal_conv for single tokens: row r of x [batch, d] continues slot index[r] (int32; None: slot r) of cache
-    [slots, k-1, d], which is moved on in place, or into the same slots of cache_out.  index[r] = -1 skips the row (its
-    y is zero).  A slot outside the cache, or one that an earlier row names, is skipped too; with check=True the call
+    [slots, k-1, d], which is moved on in place, or into the same slots of cache_out; no other tensor may overlap the
+    one that is written.  index[r] = -1 skips the row (its y is zero).  A slot outside the cache, or one that an earlier row names, is skipped too; with check=True the call
     synchronises once and raises SlotError for it.  Returns y [batch, d]."""
     code, dt, dev = _element_code("x", x), x.dtype, x.device
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
@@ -1361,7 +1371,10 @@ def causal_conv_step(cache, x, weight, bias=None, *, silu=False, index=None, cac
                              _like("bias", bias, dt, dev, (d,)), _like("cache", cache, dt, dev, (slots, k - 1, d)),
                              x_row, y_row, _like("cache_out", new, dt, dev, (slots, k - 1, d)), yp, at,
                              0 if info is None else info.data_ptr())
-    _check(lib().selinv_causal_conv_step(packed, _raw_stream(dev)), "selinv_causal_conv_step")
+    st = lib().selinv_causal_conv_step(packed, _raw_stream(dev))
+    if st == ERR_INVALID_ARG:
+        _off_cache(new, (("x", x), ("weight", weight), ("bias", bias), ("index", index)))
+    _check(st, "selinv_causal_conv_step")
     _raise_on_slots(info)
     return y
 
@@ -1499,8 +1512,8 @@ def selective_scan_ad(x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=
 def selective_scan_step(cache, x, dt, A, B, C, D=None, *, z=None, dt_bias=None, softplus=False, index=None,
                         cache_out=None, check=True, out=None):
     """selective_scan for single tokens: row r of x, dt, z [batch, d] and B, C [batch, groups, n] continues slot
-    index[r] (int32; None: slot r) of cache [slots, d, n], in place or into the same slots of cache_out.  index[r] = -1
-    skips the row (its y is zero).  A slot outside the cache, or one that an earlier row names, is skipped too; with
+    index[r] (int32; None: slot r) of cache [slots, d, n], in place or into the same slots of cache_out; no other tensor
+    may overlap the one that is written.  index[r] = -1 skips the row (its y is zero).  A slot outside the cache, or one that an earlier row names, is skipped too; with
     check=True the call synchronises once and raises SlotError for it.  Returns y [batch, d]."""
     code, ty, dev, ct = _element_code("x", x), x.dtype, x.device, _arith(x.dtype)
     if x.dim() != 2 or not isinstance(A, torch.Tensor) or A.dim() != 2 or not isinstance(B, torch.Tensor) or B.dim() != 3:
@@ -1530,6 +1543,10 @@ def selective_scan_step(cache, x, dt, A, B, C, D=None, *, z=None, dt_bias=None, 
                              _like("A", A, ct, dev, (d, n)), _like("D", D, ct, dev, (d,)),
                              _like("dt_bias", dt_bias, ct, dev, (d,)), _like("cache", cache, ct, dev, (slots, d, n)),
                              _like("cache_out", new, ct, dev, (slots, d, n)), yp, at, 0 if info is None else info.data_ptr())
-    _check(lib().selinv_selective_scan_step(packed, _raw_stream(dev)), "selinv_selective_scan_step")
+    st = lib().selinv_selective_scan_step(packed, _raw_stream(dev))
+    if st == ERR_INVALID_ARG:
+        _off_cache(new, (("x", x), ("dt", dt), ("z", z), ("B", B), ("C", C), ("A", A), ("D", D), ("dt_bias", dt_bias),
+                         ("index", index)))
+    _check(st, "selinv_selective_scan_step")
     _raise_on_slots(info)
     return y

@@ -54,3 +54,26 @@ int main()
     subprocess.check_call(["g++", "-std=c++17", "-fsanitize=signed-integer-overflow", "-fno-sanitize-recover", "-I",
                            build.CSRC, str(src), "-o", str(exe)])
     assert subprocess.check_output([str(exe)]).decode().strip() == "0"
+
+
+def test_steps_refuse_arrays_in_the_cache_that_is_written(lib):
+    """Addresses alone decide; what passes them is not called here."""
+    from tests.test_sequence_abi import step
+    cache = FAKE + (1 << 20)                # 3 slots x 6 channels x 4 states: 288 bytes
+    apart = dict(cache=cache, out=cache)
+    for at in (cache, cache + 284, cache - 4):
+        for key in ("x", "dt", "z", "B", "C", "y", "A", "D", "bias", "index", "info"):
+            assert lib.selinv_selective_scan_step(step(**{**apart, key: at}), 0) == selinv.ERR_INVALID_ARG, key
+    for at in (cache + 4, cache - 284):
+        assert lib.selinv_selective_scan_step(step(cache=at, out=cache), 0) == selinv.ERR_INVALID_ARG
+
+    def conv(**change):
+        v = dict(dtype=selinv.F32, flags=0, batch=3, slots=3, d=6, k=4, x=FAKE, weight=FAKE, bias=0, cache=cache, xr=6, yr=6,
+                 out=cache, y=FAKE, index=0, info=0)        # 3 slots x 3 rows x 6 channels: 216 bytes
+        v.update(change)
+        return lib.selinv_causal_conv_step(selinv._CONV_STEP.pack(*v.values()), 0)
+
+    for at in (cache, cache + 212, cache - 4):
+        for key in ("x", "weight", "bias", "y", "index", "info"):
+            assert conv(**{key: at}) == selinv.ERR_INVALID_ARG, key
+    assert conv(cache=cache + 4) == selinv.ERR_INVALID_ARG

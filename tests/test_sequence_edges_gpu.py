@@ -408,3 +408,36 @@ def test_missing_tensors_are_refused(cuda_ok):
         selinv.causal_conv_step(cache, x[:, 0], w, cache_out=[1.0])
     with pytest.raises(ValueError):
         selinv.causal_conv(x[0], w, plan=[4, 2])
+
+
+def test_steps_whose_inputs_lie_in_the_cache_are_refused(cuda_ok):
+    """Rows are done in no order, so an input that another row's new state replaces is no input.  What lies beside the
+    cache, or in a cache that is only read, is one."""
+    whole = torch.randn(6, 3, 8, device="cuda")
+    cache, w = whole[:4], torch.ones(8, 4, device="cuda")
+    index = torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda")
+    x = torch.randn(3, 8, device="cuda")
+    conv = lambda x, c=cache, w=w, i=index, **k: selinv.causal_conv_step(c, x, w, index=i, **k)     # noqa: E731
+    for bad in (dict(x=cache[1:, -1]), dict(x=cache[:3, 0], cache_out=cache), dict(x=whole[3:, 0]),
+                dict(x=x, w=cache.view(-1)[:32].view(8, 4)), dict(x=x, i=cache.view(torch.int32).view(-1)[:3])):
+        with pytest.raises(ValueError, match="overlap"):
+            conv(**bad)
+    before = cache.clone()
+    other = torch.zeros_like(cache)
+    y = conv(cache[:3, -1].clone(), cache_out=other)
+    assert torch.equal(conv(cache[:3, -1], cache_out=other.clone()), y) and torch.equal(cache, before)
+    conv(whole[4:, 0].expand(2, 8)[[0, 1, 0]])
+    conv(torch.empty_strided((3, 8), (24, 1), device="cuda").copy_(x))
+    v, _, _ = scan_inputs(40, torch.float32, (3, 1), 8, 2, 2)
+    a = {k: b[:, 0] if k in ("x", "dt", "B", "C", "z") else b for k, b in v.items() if k != "state"}
+    states = torch.randn(5, 8, 2, device="cuda")
+    flat = states.view(-1)
+    part = {"x": flat[8:32].view(3, 8), "dt": flat[56:80].view(3, 8), "B": flat[2:14].view(3, 2, 2),
+            "C": flat[-12:].view(3, 2, 2), "A": states[1], "z": flat[:24].view(3, 8), "D": flat[70:78], "dt_bias": flat[:8]}
+    for k, bad in part.items():
+        with pytest.raises(ValueError, match=f"^{k} must not overlap"):
+            selinv.selective_scan_step(states, **{**a, k: bad}, index=index)
+        ok = selinv.selective_scan_step(states, **{**a, k: bad}, index=index, cache_out=torch.empty_like(states))
+        assert torch.equal(ok, selinv.selective_scan_step(states.clone(), **{**a, k: bad.clone()}, index=index)), k
+    assert selinv.selective_scan_step(states, **{k: b[:0] if k in ("x", "dt", "B", "C", "z") else b
+                                                 for k, b in a.items()}).shape == (0, 8)
