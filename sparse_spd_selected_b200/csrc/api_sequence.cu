@@ -235,7 +235,7 @@ selinv_status conv_check(const selinv_conv_inputs &a)
 
 // Rows per thread: enough threads to keep every SM's loads in flight, but chunks long enough that the K - 1 rows before
 // each cost little.
-int64_t conv_chunk(const selinv_conv_inputs &a, bool backward)
+int64_t conv_chunk(const selinv_conv_inputs &a)
 {
     const int64_t per = a.dtype == SELINV_F64 ? 2 : 4, vecs = div_up(a.d, per) * (a.lines > 0 ? a.lines : 1);
     const int64_t want = 1024 * (int64_t)sm_count(), least = 16, most = 128;
@@ -245,11 +245,11 @@ int64_t conv_chunk(const selinv_conv_inputs &a, bool backward)
 }
 size_t conv_space(const selinv_conv_inputs &a)
 {
-    const int64_t chunks = div_up(a.rows, conv_chunk(a, true));
+    const int64_t chunks = div_up(a.rows, conv_chunk(a));
     return round_up((size_t)a.lines * (chunks > 1 ? chunks : 1) * (a.k + 1) * a.d * arith(a.dtype));
 }
 
-selinv_status conv_args(const selinv_conv_inputs &a, bool backward, ConvArgs &p)
+selinv_status conv_args(const selinv_conv_inputs &a, ConvArgs &p)
 {
     const size_t es = elem(a.dtype);
     p.rows = Rows{a.table, (int)a.live, (int)a.rows};
@@ -258,7 +258,7 @@ selinv_status conv_args(const selinv_conv_inputs &a, bool backward, ConvArgs &p)
     p.silu = a.flags & SELINV_SILU;
     p.x = in_of(a.x, es, 0);
     p.weight = a.weight, p.bias = a.bias, p.state = a.state;
-    p.chunk_rows = (int)conv_chunk(a, backward);
+    p.chunk_rows = (int)conv_chunk(a);
     const int64_t chunks = div_up(a.rows, p.chunk_rows);
     if (div_up(div_up(a.d, es == 8 ? 2 : 4) * a.lines * chunks, 128) > MAX_GRID_X) return SELINV_ERR_UNSUPPORTED;
     p.chunks = (int)(chunks > 1 ? chunks : 1);
@@ -409,7 +409,7 @@ selinv_status selinv_causal_conv(const selinv_conv_inputs *a, const selinv_view 
         return copy_states(state_out, a->state, (size_t)a->lines * a->d * (a->k - 1) * es, s);
     if (a->rows > 0 && !view_ok(*y, es)) return SELINV_ERR_INVALID_ARG;
     ConvArgs p{};
-    st = conv_args(*a, false, p);
+    st = conv_args(*a, p);
     if (st != SELINV_OK) return st;
     p.y = out_of(*y, es, 0);
     p.state_out = state_out;
@@ -435,7 +435,7 @@ selinv_status selinv_causal_conv_backward(const selinv_conv_inputs *a, const sel
     if (a->rows > 0 && (!view_ok(g->yb, es) || !view_ok(g->xb, es))) return SELINV_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < conv_space(*a)) return SELINV_ERR_WORKSPACE;
     ConvArgs p{};
-    st = conv_args(*a, true, p);
+    st = conv_args(*a, p);
     if (st != SELINV_OK) return st;
     p.yb = in_of(g->yb, es, 0);
     p.xb = out_of(g->xb, es, 0);

@@ -87,19 +87,6 @@ template <int N> SELINV_DEVINL void get(const double *p, double2 *v)
     for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const double2 *>(p + 2 * i);
 }
 
-template <int N> SELINV_DEVINL void put(float *p, const float2 *v)
-{
-    float t[2 * N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) t[2 * i] = v[i].x, t[2 * i + 1] = v[i].y;
-    put<2 * N>(p, t);
-}
-template <int N> SELINV_DEVINL void put(double *p, const double2 *v)
-{
-#pragma unroll
-    for (int i = 0; i < N; ++i) *reinterpret_cast<double2 *>(p + 2 * i) = v[i];
-}
-
 // Starts copying CW channels (nch of them exist) of rows r .. r1 - 1, at most SCAN_R, into `to`.  FULL: all channels, all
 // rows, on 16 bytes; straight code, since a few warps wait for nothing but their own instructions here.
 template <int CW, bool FULL, class T>

@@ -253,7 +253,7 @@ SELINV_DEVINL double2 exp2_2(double2 e) { return make_double2(exp2(e.x), exp2(e.
 SELINV_DEVINL float2 decay2(float2 dt, float2 A2) { return exp2_2(fma2(dt, A2, make_float2(1.8e-8f, 1.8e-8f))); }
 SELINV_DEVINL double2 decay2(double2 dt, double2 A2) { return exp2_2(mul2(dt, A2)); }
 
-// 1 / (1 + e^-x).
+// 1 / (1 + e^-x): in float to 7 units in the last place and, where e^-x counts, the 1.3 |x| of its rounded argument.
 SELINV_DEVINL float sigmoid_(float x) { return rcp_(1.0f + exp2_(-log2e<float>() * x)); }
 SELINV_DEVINL double sigmoid_(double x) { return 1.0 / (1.0 + exp(-x)); }
 SELINV_DEVINL float2 sigmoid2(float2 x)
@@ -275,12 +275,12 @@ SELINV_DEVINL float2 silu_slope2(float2 x, float2 p)
 SELINV_DEVINL double2 silu_slope2(double2 x, double2 p) { return make_double2(silu_slope(x.x, p.x), silu_slope(x.y, p.y)); }
 
 // log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].  In float log1p(e) = e + e^2 r(e), r of degree 7, minimax
-// for the relative error by Remez's exchange (3.3e-8; 6.0e-8 with float coefficients): log(1 + e) itself would lose e's low bits for far negative x, and would use
-// the special function unit, which bounds the scan, a second time.  There the result is e, whose argument, up to 125, must
-// not be rounded: with EXACT what the product and log2 e lose is put back into e, and the result is good to some 10
-// units in its last place over the whole range (up to |x| = 256, from where on e is nothing).  Without, 1.3 |x| units are
-// added to them, nothing to steps that come from 16-bit inputs and lead to 16-bit outputs (EXACT for those too: 1288 us
-// for 1275, 4 x 2048 x 4096 x 16 forward and backward).
+// for the relative error by Remez's exchange (3.3e-8; 6.0e-8 with float coefficients): log(1 + e) itself would lose e's
+// low bits for far negative x, and would use the special function unit, which bounds the scan, a second time.  There the
+// result is e, whose argument, up to 125, must not be rounded: with EXACT what the product and log2 e lose is put back into
+// e, and the result is good to some 10 units in its last place over the whole range (from |x| = 256 on e is nothing).
+// Without, 1.3 |x| units are added to them, nothing to steps that come from 16-bit inputs and lead to 16-bit outputs
+// (EXACT for those too: 1288 us for 1275, 4 x 2048 x 4096 x 16 forward and backward).
 SELINV_DEVINL float max_nan(float a, float b)
 {
     float r;

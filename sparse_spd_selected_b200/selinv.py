@@ -1352,8 +1352,9 @@ def _raise_on_slots(info):
 def causal_conv_step(cache, x, weight, bias=None, *, silu=False, index=None, cache_out=None, check=True, out=None):
     """causal_conv for single tokens: row r of x [batch, d] continues slot index[r] (int32; None: slot r) of cache
     [slots, k-1, d], which is moved on in place, or into the same slots of cache_out; no other tensor may overlap the
-    one that is written.  index[r] = -1 skips the row (its y is zero).  A slot outside the cache, or one that an earlier row names, is skipped too; with check=True the call
-    synchronises once and raises SlotError for it.  Returns y [batch, d]."""
+    one that is written.  index[r] = -1 skips the row (its y is zero).  A slot outside the cache, or one that an earlier
+    row names, is skipped too; with check=True the call synchronises once and raises SlotError for it.  Returns y
+    [batch, d]."""
     code, dt, dev = _element_code("x", x), x.dtype, x.device
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be [batch, d] and weight [d, k]")
@@ -1513,8 +1514,9 @@ def selective_scan_step(cache, x, dt, A, B, C, D=None, *, z=None, dt_bias=None, 
                         cache_out=None, check=True, out=None):
     """selective_scan for single tokens: row r of x, dt, z [batch, d] and B, C [batch, groups, n] continues slot
     index[r] (int32; None: slot r) of cache [slots, d, n], in place or into the same slots of cache_out; no other tensor
-    may overlap the one that is written.  index[r] = -1 skips the row (its y is zero).  A slot outside the cache, or one that an earlier row names, is skipped too; with
-    check=True the call synchronises once and raises SlotError for it.  Returns y [batch, d]."""
+    may overlap the one that is written.  index[r] = -1 skips the row (its y is zero).  A slot outside the cache, or one
+    that an earlier row names, is skipped too; with check=True the call synchronises once and raises SlotError for it.
+    Returns y [batch, d]."""
     code, ty, dev, ct = _element_code("x", x), x.dtype, x.device, _arith(x.dtype)
     if x.dim() != 2 or not isinstance(A, torch.Tensor) or A.dim() != 2 or not isinstance(B, torch.Tensor) or B.dim() != 3:
         raise ValueError("x must be [batch, d], A [d, n] and B [batch, groups, n]")

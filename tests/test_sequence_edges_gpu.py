@@ -6,7 +6,7 @@ import torch
 
 from sparse_spd_selected_b200 import selinv
 from tests import sequence_plain as plain
-from tests.test_sequence_gpu import TYPES, arith, dev, host, near, scan_inputs, unit
+from tests.test_sequence_gpu import TYPES, arith, check_scan, dev, host, near, scan_inputs, unit
 
 pytestmark = pytest.mark.gpu
 
@@ -441,3 +441,21 @@ def test_steps_whose_inputs_lie_in_the_cache_are_refused(cuda_ok):
         assert torch.equal(ok, selinv.selective_scan_step(states.clone(), **{**a, k: bad.clone()}, index=index)), k
     assert selinv.selective_scan_step(states, **{k: b[:0] if k in ("x", "dt", "B", "C", "z") else b
                                                  for k, b in a.items()}).shape == (0, 8)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("lines,rows,d,n,cut", [
+    # blocks of the forward at one lane per channel, on 148 multiprocessors: 258, 157 and 213 leave lines whole, with one
+    # lane, two and two
+    (2, 18, 16400, 16, False), (1, 18, 20001, 16, False), (3, 18, 9000, 7, False),
+    # 112, 60 and 3 have them cut, with one lane, two and four
+    (1, 260, 14300, 5, True), (1, 260, 7600, 9, True), (1, 150, 300, 16, True),
+    # more states: no fewer than two lanes, or four
+    (1, 150, 300, 20, True), (1, 150, 70, 40, True), (2, 18, 2400, 33, False),
+])
+def test_scan_dispatch(cuda_ok, kind, lines, rows, d, n, cut):
+    """Sizes on each side of the rules that choose lanes and segments, with channels that end inside a tile."""
+    shape = selinv._SCAN_INPUTS.pack(selinv.F32 if kind == "f32" else selinv.BF16, 0, lines, rows, d, n, 1, 0, 0, 0,
+                                     *[0, 0, 0] * 5, 0, 0, 0, 0, 0, 0)
+    assert (selinv.lib().selinv_selective_scan_workspace_size(shape) > 0) == cut
+    check_scan(41, kind, [rows] * lines, d, n, with_state=True)
