@@ -21,9 +21,11 @@
 // Bounded by the issue of instructions and their latency: a warp of 32 channels
 // takes about 370 per row, at 255 registers two warps per scheduler hide part of
 // each other's waits (0.45 instructions a cycle).  4 x 2048 x 4096 x 16 in
-// bfloat16: 963 us, of which 178 the run over the segments' ends and 13 the
+// bfloat16: 969 us, of which 180 the run over the segments' ends and 14 the
 // partial sums, against 137 us for the powers of two and sigmoids of one pass
-// and 92 us of memory.  Keeping the first run's powers for the second would take
+// and 92 us of memory.  Three quarters of the rows' states are formed twice, and
+// at 255 registers a thread spills 72 bytes of stores and 356 of loads (float64
+// up to 476 and 996).  Keeping the first run's powers for the second would take
 // 32 KB a warp, and so half of the warps.
 #pragma once
 
@@ -126,21 +128,22 @@ template <class K> struct ScanBwd {
         }
     }
     // SCAN_S rows of the first run.  EDGE: some row begins a sequence.
-    template <bool EDGE> SELINV_DEVINL void skip(int t0, uint32_t begins, int k0, const V (*A2)[KP], V (*h)[KP]) const
+    template <bool EDGE, bool REAL> SELINV_DEVINL void skip(int t0, uint32_t begins, int k0, const V (*A2)[KP], V (*h)[KP]) const
     {
 #pragma unroll
         for (int r = 0; r < SCAN_S; ++r) {
             V a[2][KP];
             if (EDGE && ((begins >> (t0 + r)) & 1u)) states(p.state, sequence(k0, begins, t0 + r), h);
-            row<false>(t0 + r, A2, h, a);
+            row<REAL>(t0 + r, A2, h, a);
         }
     }
-    // Rows t0 .. t0 + S - 1, `before` the state before them.  EDGE: some row begins or ends a sequence; st has the
+    // Rows t0 .. t0 + SCAN_S - 1, `before` the state before them.  EDGE: some row begins or ends a sequence; st has the
     // rows that begin one and the row behind the last, of which only those below nr are rows.
-    template <int S, bool EDGE, bool REAL>
+    template <bool EDGE, bool REAL>
     SELINV_DEVINL void rows(int t0, int nr, uint32_t st, int k0, const V (*A2)[KP], const V (*before)[KP], V (*g)[KP],
                             V (*ab)[KP]) const
     {
+        constexpr int S = SCAN_S;
         const uint32_t begins = st & ((1u << nr) - 1u);
         V h[S][2][KP], a[S][2][KP];
 #pragma unroll
@@ -215,9 +218,9 @@ template <class K> struct ScanBwd {
                 out[SN + 2 * j] = sc[j].x, out[SN + 2 * j + 1] = sc[j].y;
             }
 #pragma unroll
-            for (int i = 0; i < K::CHUNKS; ++i) put<K::Q>(&sm.part[S > 1 ? r % K::P : t % K::P][nl][i][lane % K::LD][0], out + i * K::Q);
+            for (int i = 0; i < K::CHUNKS; ++i) put<K::Q>(&sm.part[r % K::P][nl][i][lane % K::LD][0], out + i * K::Q);
             if (first && o.stateb_out) store(static_cast<C *>(o.stateb_out) + p.rows.number(sequence(k0, st, t), line) * dn, g);
-            if ((S > 1 ? r : t) % K::P == 0) {
+            if (r % K::P == 0) {
                 __syncwarp();
                 sums(t);
                 __syncwarp();
@@ -225,6 +228,7 @@ template <class K> struct ScanBwd {
         }
     }
     // The nr rows of a tile, from the state kept before them; begins and st as above.
+    template <bool REAL>
     SELINV_DEVINL void tile(const C *kept, int nr, uint32_t begins, uint32_t st, int k0, const V (*A2)[KP], V (*g)[KP],
                             V (*ab)[KP]) const
     {
@@ -232,10 +236,10 @@ template <class K> struct ScanBwd {
         V h[2][KP];
         load(kept, h);
         for (int b = 0; b < SCAN_R / S - 1 && (b + 1) * S < nr; ++b) {
-            if ((begins >> (b * S)) & ((1u << S) - 1u))
-                skip<true>(b * S, begins, k0, A2, h);
+            if (REAL || ((begins >> (b * S)) & ((1u << S) - 1u)))
+                skip<true, REAL>(b * S, begins, k0, A2, h);
             else
-                skip<false>(b * S, begins, k0, A2, h);
+                skip<REAL, REAL>(b * S, begins, k0, A2, h);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -250,27 +254,10 @@ template <class K> struct ScanBwd {
             } else {
                 load(kept, h);
             }
-            if ((st >> (b * S)) & ((2u << S) - 1u))
-                rows<S, true, false>(b * S, nr, st, k0, A2, h, g, ab);
+            if (REAL || ((st >> (b * S)) & ((2u << S) - 1u)))
+                rows<true, REAL>(b * S, nr, st, k0, A2, h, g, ab);
             else
-                rows<S, false, false>(b * S, nr, st, k0, A2, h, g, ab);
-        }
-    }
-    // The same with zeros for what does not exist, row by row, each from the kept state: slow, but little code.
-    SELINV_DEVINL void real_tile(const C *kept, int nr, uint32_t begins, uint32_t st, int k0, const V (*A2)[KP], V (*g)[KP],
-                                V (*ab)[KP]) const
-    {
-#pragma unroll 1
-        for (int t = nr - 1; t >= 0; --t) {
-            V h[2][KP];
-            load(kept, h);
-#pragma unroll 1
-            for (int s = 0; s < t; ++s) {
-                V a[2][KP];
-                if ((begins >> s) & 1u) states(p.state, sequence(k0, begins, s), h);
-                row<true>(s, A2, h, a);
-            }
-            rows<1, true, true>(t, nr, st, k0, A2, h, g, ab);
+                rows<REAL, REAL>(b * S, nr, st, k0, A2, h, g, ab);
         }
     }
     // Bb's and Cb's sums over this warp's channels for rows t .. t + P - 1: a pair of states at a time, from another
@@ -462,10 +449,7 @@ SELINV_DEVINL bool scan_backward_block(const ScanArgs &p, const ScanGrads &o, ch
         __syncthreads();
 
         const C *kept = static_cast<const C *>(o.kept) + (w.line * tiles + rt / R) * dn;
-        if constexpr (REAL)
-            at.real_tile(kept, nr, begins, st, k0, A2, g, ab);
-        else
-            at.tile(kept, nr, begins, st, k0, A2, g, ab);
+        at.template tile<REAL>(kept, nr, begins, st, k0, A2, g, ab);
         __syncwarp();
         // finish the rows, four of a lane's at a time: all loads, then the arithmetic, then the stores
         constexpr int F = PER < 4 ? PER : 4;
@@ -567,9 +551,9 @@ SELINV_DEVINL bool scan_backward_block(const ScanArgs &p, const ScanGrads &o, ch
     return __syncthreads_or(probe != (C)0);
 }
 // PADDED: some states or channels of the blocks do not exist.  Where something is not finite the block then begins again: what
-// tells is in no tile's way, and not in the kernel that has no use for it (4 x 2048 x 4096 in bfloat16, backward: 979 us
-// with 12 states, 955 without any of this; 16 states, all there, 968.  Told apart tile by tile, inside the loop, its
-// registers cost those 60 us.)
+// tells is in no tile's way, and not in the kernel that has no use for it (4 x 2048 x 4096 in bfloat16, backward: 987 us
+// with 12 states, 955 without any of this, 1062 with infinities in one channel; 16 states, all there, 969.  Told apart
+// tile by tile, inside the loop, its registers cost those 60 us.)
 template <class K, bool PADDED>
 __global__ void __launch_bounds__(SCAN_WARPS * 32, scan_bwd_blocks<K>)
     scan_backward_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ ScanGrads o)

@@ -72,7 +72,9 @@ SELINV_DEVINL typename K::C scan_row(const ScanFwdSmem<K> &sm, int t, int dl, in
 // BLOCKS per SM that the registers are kept to.  Four (128 registers), as many as segments are planned for, where they
 // fill the GPU (4096 x 2048 x 16: 121 us, 132 without); none where no more than two come to an SM, whose warps work
 // better with all they want (4 x 2048 x 4096 x 16, one lane: 358 us, 404 with).
-template <class K, bool MAIN, int BLOCKS>
+// PADDED: some of a tile's states do not exist.  A tile with infinities then goes on row by row with zeros for them; a kernel of
+// its own, since the choice costs the others 3 % (4 x 2048 x 4096 x 8 in bfloat16: 234 us for 226).
+template <class K, bool MAIN, int BLOCKS, bool PADDED>
 __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __grid_constant__ ScanArgs p)
 {
     using T = typename K::T;
@@ -143,7 +145,6 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
         if (MAIN) raw_clear_n<32>(sm.raw[i].c, p.n, lane);
     }
     C total = 0;
-    const bool padded = MAIN && p.n != K::NP;       // some states do not exist
 
     for (int rt = w.r0 - R; rt < w.r1; rt += R) {       // the first time only to fetch: one place in the code that does
         const int at = ((rt - w.r0) / R) & 1;
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
                 sm.u[t][dl] = v[i] * u[i];
                 if (!MAIN && t < nr) total += v[i];
             }
-            if (padded) {       // an infinite step makes this not finite too
+            if constexpr (PADDED) {     // an infinite step makes this not finite too
                 C probe = 0;
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
             }
             const uint32_t later = st >> (t + 1);
             const int te = later ? min(nr, t + __ffs(later)) : nr;
-            for (; finite && t + 4 <= te; t += 4) {     // four rows' loads before their stores
+            for (; (!PADDED || finite) && t + 4 <= te; t += 4) {        // four rows' loads before their stores
                 C v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = scan_row<K, MAIN, false>(sm, t + i, dl, n0, n, A2, h);
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
                 }
             }
             for (; t < te; ++t) {
-                C v[1] = {scan_row<K, MAIN, MAIN>(sm, t, dl, n0, n, A2, h)};
+                C v[1] = {scan_row<K, MAIN, PADDED>(sm, t, dl, n0, n, A2, h)};
                 if (MAIN) {
                     scatter_sum<1, CW, 32>(v, lane);
                     if (LN > 1) __syncwarp();
@@ -265,13 +266,13 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32, BLOCKS) scan_kernel(const __g
     }
 }
 
-template <class K, bool MAIN, int BLOCKS>
+template <class K, bool MAIN, int BLOCKS, bool PADDED>
 cudaError_t scan_start(const ScanArgs &p, const dim3 &grid, int threads, int bytes, cudaStream_t s)
 {
     const cudaError_t e =
-        cudaFuncSetAttribute(scan_kernel<K, MAIN, BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        cudaFuncSetAttribute(scan_kernel<K, MAIN, BLOCKS, PADDED>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    scan_kernel<K, MAIN, BLOCKS><<<grid, threads, bytes, s>>>(p);
+    scan_kernel<K, MAIN, BLOCKS, PADDED><<<grid, threads, bytes, s>>>(p);
     return cudaGetLastError();
 }
 template <class K> cudaError_t scan_run(const ScanArgs &p, cudaStream_t s)
@@ -283,11 +284,15 @@ template <class K> cudaError_t scan_run(const ScanArgs &p, cudaStream_t s)
     const dim3 grid((unsigned)(p.lines * p.segs), (unsigned)(p.groups * ((tiles + warps - 1) / warps)));
     constexpr int full = sizeof(typename K::C) == 4 ? 4 : 1;
     if (p.segs > 1) {
-        const cudaError_t e = scan_start<K, false, full>(p, grid, warps * 32, bytes, s);
+        const cudaError_t e = scan_start<K, false, full, false>(p, grid, warps * 32, bytes, s);
         if (e != cudaSuccess) return e;
     }
-    if (full > 1 && (int64_t)grid.x * grid.y <= 2 * p.sms) return scan_start<K, true, 1>(p, grid, warps * 32, bytes, s);
-    return scan_start<K, true, full>(p, grid, warps * 32, bytes, s);
+    const auto start = [&](auto blocks) {
+        return p.n != K::NP ? scan_start<K, true, blocks.value, true>(p, grid, warps * 32, bytes, s)
+                            : scan_start<K, true, blocks.value, false>(p, grid, warps * 32, bytes, s);
+    };
+    if (full > 1 && (int64_t)grid.x * grid.y <= 2 * p.sms) return start(std::integral_constant<int, 1>());
+    return start(std::integral_constant<int, full>());
 }
 
 // Calls f with the tile of NP states and so many lanes per channel.

@@ -4,8 +4,9 @@
 // y); for the states LN neighbouring lanes take their LN channels one after
 // another, four states of each a lane, so that the loads and stores of 16
 // bytes cover whole sectors.  192 rows of 4096 x 16: 28 us for 107 MB, 3.8 TB/s
-// (0.58 of a plain copy's rate); held to 64 registers for eight blocks per SM it
-// took 30.  One row of 2048 x 16: 4.7 us, a launch and two waits for memory.
+// (0.58 of a plain copy's rate); every row's blocks read A again, as many bytes
+// as the states, from L2.  Held to 64 registers for eight blocks per SM it took
+// 30.  One row of 2048 x 16: 4.7 us, a launch and two waits for memory.
 #pragma once
 
 #include "conv.cuh"
